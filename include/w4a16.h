@@ -3,6 +3,9 @@
  *
  * Block-scaled 4-bit weight-only linear layers: pack BF16 weight matrices to
  * NVFP4 or ROCmFP4, then multiply BF16 activations by the packed weights.
+ * Layers with both operands in 4 bits (W4A4): quantise activations to MXFP4 or
+ * NVFP4, multiply them by packed weights, and run the norms, the gate and the
+ * residual between two such layers in one pass.
  *
  * Sources (web pages on the subject):
  *   [EdgeRock]  "EdgeRock-4B-NVFP4" model card, intro: the W4A16 NVFP4 format --
@@ -59,7 +62,8 @@ typedef enum {
     W4_FMT_NVFP4 = 1,         /* [EdgeRock] E2M1 + E4M3 per 16 + FP32 global */
     W4_FMT_ROCMFP4_DUAL = 2,  /* [rocmwhy] 18-byte blocks, two half scales   */
     W4_FMT_ROCMFP4_FAST = 3,  /* [rocmwhy] 17-byte blocks, one scale         */
-    W4_FMT_Q4_0 = 4           /* [rocmwhy] table: stock Q4_0, for comparison  */
+    W4_FMT_Q4_0 = 4,          /* [rocmwhy] table: stock Q4_0, for comparison  */
+    W4_FMT_MXFP4 = 5          /* OCP MX: E2M1 + one power of two per 32 (W4A4 only) */
 } w4_format;
 
 typedef enum {
@@ -319,6 +323,143 @@ size_t w4a16_workspace_bytes(const w4_weights *w, int M);
  */
 #define W4_NOALLOC_SCRATCH_BYTES (8u << 20)
 w4_status w4a16_gemv_noalloc(const w4_weights *w, const void *x, int M, float *y, void *stream);
+
+/* ------------------------------------------------------ 4-bit activations --- */
+
+typedef enum { W4_TYPE_BF16 = 0, W4_TYPE_F16 = 1, W4_TYPE_F32 = 2 } w4_type;
+
+typedef enum {
+    W4_MX_SCALE_FLOOR = 0,  /* 2^(floor(log2 amax) - 2) (OCP MX 1.0, 6.3): values above 6 scales saturate */
+    W4_MX_SCALE_CEIL = 1    /* smallest power of two with amax <= 6 scales: nothing saturates (MXFP4 only) */
+} w4_mx_scale;
+
+/*
+ * A block-scaled 4-bit operand of the W4A4 product: `rows` rows (tokens, or the
+ * output features of a weight matrix) of K values, K % 32 == 0 (all pointers
+ * device memory, owned by the caller).
+ *   fmt     W4_FMT_MXFP4: blocks of 32 values, scale = E8M0 byte b, 2^(b - 127)
+ *           (0xFF: NaN).  W4_FMT_NVFP4: blocks of 16 values, scale = E4M3 byte
+ *           (0x7F: NaN), times the global scale.
+ *   codes   [rows][K/2] bytes, E2M1 nibbles as in w4_weights.
+ *   scales  fp4_scale_bytes(fmt, rows, K) bytes: 4 consecutive scales of a row
+ *           are one word; word j of row r is at byte
+ *           ((r / 128) * T + j) * 512 + (r % 32) * 16 + ((r % 128) / 32) * 4,
+ *           T = ceil(scales per row / 4).  Scales past the end of a row in its
+ *           last word are 0; rows past the last are not read or written.
+ *   global_scale  NVFP4: one float.  MXFP4: not read (may be NULL).
+ * value = e2m1 * scale (* global scale).
+ */
+typedef struct {
+    int fmt;
+    int rows;
+    int K;
+    const uint8_t *codes;
+    const uint8_t *scales;
+    const float *global_scale;
+} w4_fp4;
+
+/* Bytes of the scale tiles of an operand (0 for a bad format or shape). */
+size_t fp4_scale_bytes(int fmt, int rows, int K);
+
+/*
+ * fp4_quantize -- quantise rows of activations (or weights) to a 4-bit operand.
+ *   MXFP4: per 32 values e = floor(log2 amax) - 2, at least -127 (or by
+ *          W4_MX_SCALE_CEIL); code = E2M1(x * 2^-e), nearest even, saturating
+ *          at 6, sign kept.
+ *   NVFP4: per 16 values, with the given global scale g (finite, >= 0):
+ *          s = E4M3(amax / 6 / g) as in pack_nvfp4, code = E2M1(x * RN(1 / (s * g))),
+ *          binary32.  A block whose 1 / (s * g) is not finite becomes zeros.
+ *   A block that holds Inf or NaN gets the NaN scale: every value it stands for
+ *   is NaN, and so is every product with its row.
+ *   x        [rows] rows of K values of `type` (w4_type), `ldx` >= K values apart;
+ *            x and every row start on 16 bytes.
+ *   codes, scales   out, as in w4_fp4.
+ *   d_status optional device int: set to W4_OK at the start of the call,
+ *            W4_ERR_NONFINITE if x holds Inf or NaN.
+ */
+w4_status fp4_quantize(const void *x, int type, long long ldx, int rows, int K, int fmt, int scale_rule,
+                       const float *global_scale, uint8_t *codes, uint8_t *scales, int *d_status,
+                       void *stream);
+
+/*
+ * fp4_dequantize -- the values an operand stands for, rounded to `type` (MXFP4
+ * values are exact in BF16 and binary32): out [rows] rows of K values, `ldo` >= K
+ * values apart, every row on 16 bytes.
+ */
+w4_status fp4_dequantize(const w4_fp4 *a, void *out, int type, long long ldo, void *stream);
+
+/*
+ * fp4_tile_scales -- lay out row-major scales [rows][K/32 (MXFP4) | K/16 (NVFP4)]
+ * (a pack_nvfp4 result, a checkpoint) as the tiles of w4_fp4; the codes of such a
+ * matrix are used as they are.
+ */
+w4_status fp4_tile_scales(int fmt, int rows, int K, const uint8_t *row_scales, uint8_t *scales, void *stream);
+
+/*
+ * w4a4_gemm -- y[m][n] = sum_k x_hat[m][k] * w_hat[n][k] with both operands in
+ * 4 bits, on the tensor cores' block-scaled FP4 products (tcgen05.mma kind::mxf4
+ * and kind::mxf4nvf4, binary32 accumulators); any number of tokens from one.  The
+ * global scales are applied together at the end.  Deterministic.
+ *   w, x      operands of the same format and K.
+ *   y         out, x->rows rows of w->rows values of out_type (w4_type), `ldy` >=
+ *             w->rows values apart (any alignment of the rows; y on 16 bytes).
+ *   flags     0, or W4_LAUNCH_PDL: the weights may be read while the previous
+ *             kernel on the stream is still running (it must not write them); x
+ *             is read and y written only after it has completed.
+ */
+w4_status w4a4_gemm(const w4_fp4 *w, const w4_fp4 *x, void *y, int out_type, long long ldy, unsigned flags,
+                    void *stream);
+
+/*
+ * w4a4_linear -- fp4_quantize of x to w's format, then w4a4_gemm, in one call:
+ * the linear layer with 4-bit activations.
+ *   x, type, ldx, scale_rule, global_scale (of x), d_status  as for fp4_quantize.
+ *   workspace >= w4a4_workspace_bytes(w, M) bytes: the 4-bit x.  Calls whose work
+ *             may overlap need workspaces of their own.
+ */
+w4_status w4a4_linear(const w4_fp4 *w, const void *x, int type, long long ldx, int M, int scale_rule,
+                      const float *global_scale, void *y, int out_type, long long ldy, void *workspace,
+                      size_t workspace_bytes, int *d_status, void *stream);
+size_t w4a4_workspace_bytes(const w4_fp4 *w, int M);
+
+typedef enum { W4_GATE_NONE = 0, W4_GATE_SIGMOID = 1, W4_GATE_TANH = 2 } w4_gate;
+
+/*
+ * w4_block_norm -- what stands between two blocks of a decoder, in one pass over
+ * M rows of D values (1 <= D <= 32768, W4_ERR_UNSUPPORTED above):
+ *   b  = y * rsqrt(mean(y^2) + eps) * (w_post + weight_offset)   (b = y without w_post)
+ *   h' = residual_scale * h + block_scale * act(gate) * b        (no h: the second term alone)
+ *   z  = h' * rsqrt(mean(h'^2) + eps) * (w_pre + weight_offset)  (no w_pre: factor 1)
+ * in binary32, each output rounded once: z is formed from h' before h' is
+ * rounded.  y, h, the weights, the gate, h_out and z are of `type` (w4_type);
+ * rows `ld*` >= D values apart.
+ *   gate      row m / gate_rows of the gate applies to row m (gate_rows = 1: a row
+ *             each; >= M: one row for all); gate_act W4_GATE_NONE (as it is),
+ *             W4_GATE_SIGMOID or W4_GATE_TANH.
+ *   h_out     h', or NULL; may be h or y (same row distance).
+ *   z         with quant_fmt 0; may be y (same row distance).
+ *   codes, scales  with quant_fmt W4_FMT_MXFP4 or W4_FMT_NVFP4 (D % 32 == 0; z must
+ *             be NULL): z as the 4-bit operand [M][D] of w4a4_gemm, with
+ *             scale_rule, global_scale and d_status as for fp4_quantize.
+ * Tensor pointers are aligned to their type; 16-byte aligned rows with
+ * D % 8 == 0 take 16-byte accesses, others single ones.
+ */
+typedef struct {
+    int type, M, D;
+    const void *y, *h, *w_post, *w_pre, *gate;
+    long long ldy, ldh, ldgate;
+    int gate_rows, gate_act;
+    float residual_scale, block_scale, eps, weight_offset;
+    void *h_out;
+    long long ldh_out;
+    void *z;
+    long long ldz;
+    int quant_fmt, scale_rule;
+    const float *global_scale;
+    uint8_t *codes, *scales;
+    int *d_status;
+} w4_norm;
+w4_status w4_block_norm(const w4_norm *n, void *stream);
 
 /* ------------------------------------------------------------- utilities --- */
 

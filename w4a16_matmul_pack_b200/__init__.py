@@ -10,6 +10,14 @@ The functions keep the C names:
     w4a16_gemv(w, x)         -> y float32 [M][N]  (decode, M <= 16)
     w4a16_gemm(w, x)         -> (y float32, y bf16) (prefill)
 
+and, with both operands in 4 bits (MXFP4 or NVFP4):
+
+    fp4_quantize(x, fmt)     -> Fp4Tensor        (activations, or weights)
+    fp4_from_packed(w)       -> Fp4Tensor        (NVFP4 PackedWeights, codes shared)
+    w4a4_gemm(w, x)          -> y [M][N]         (any M, x an Fp4Tensor)
+    w4a4_linear(w, x)        -> y [M][N]         (quantises x, then multiplies)
+    block_norm(y, h, ...)    -> (h', z)          (post-norm, gate, residual, pre-norm; z may be an Fp4Tensor)
+
 There is no CPU fallback: if the library is missing the import of a function
 raises, and every call requires CUDA tensors.
 """
@@ -29,9 +37,12 @@ __all__ = [
     "LAUNCH_PDL", "set_wait_limit", "pack_nvfp4", "pack_rocmfp4", "w4a16_gemv", "w4a16_gemv_grouped", "w4a16_gemm",
     "w4a16_workspace_bytes", "pack_nvfp4_workspace_bytes", "w4_encode_scalars", "save_packed", "load_packed",
     "w4_device_error", "lib", "library_path",
+    "Fp4Tensor", "FMT_MXFP4", "MX_SCALE_FLOOR", "MX_SCALE_CEIL", "fp4_quantize", "fp4_dequantize", "fp4_from_rows",
+    "fp4_from_packed", "fp4_scale_bytes", "w4a4_gemm", "w4a4_linear", "w4a4_workspace_bytes", "block_norm",
 ]
 
-FMT_NVFP4, FMT_ROCMFP4_DUAL, FMT_ROCMFP4_FAST, FMT_Q4_0 = 1, 2, 3, 4
+FMT_NVFP4, FMT_ROCMFP4_DUAL, FMT_ROCMFP4_FAST, FMT_Q4_0, FMT_MXFP4 = 1, 2, 3, 4, 5
+MX_SCALE_FLOOR, MX_SCALE_CEIL = 0, 1
 SCALE_ABSMAX, SCALE_MSE = 0, 1
 LAUNCH_PDL = 1
 BLOCK_BYTES = {FMT_ROCMFP4_DUAL: 18, FMT_ROCMFP4_FAST: 17}
@@ -49,6 +60,23 @@ class W4Error(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
         super().__init__(f"{what}: {lib().w4_status_string(status).decode()}")
+
+
+class _Fp4(ctypes.Structure):
+    _fields_ = [("fmt", ctypes.c_int), ("rows", ctypes.c_int), ("K", ctypes.c_int),
+                ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("global_scale", ctypes.c_void_p)]
+
+
+class _Norm(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int) for n in ("type", "M", "D")]
+                + [(n, ctypes.c_void_p) for n in ("y", "h", "w_post", "w_pre", "gate")]
+                + [(n, ctypes.c_longlong) for n in ("ldy", "ldh", "ldgate")]
+                + [(n, ctypes.c_int) for n in ("gate_rows", "gate_act")]
+                + [(n, ctypes.c_float) for n in ("residual_scale", "block_scale", "eps", "weight_offset")]
+                + [("h_out", ctypes.c_void_p), ("ldh_out", ctypes.c_longlong),
+                   ("z", ctypes.c_void_p), ("ldz", ctypes.c_longlong),
+                   ("quant_fmt", ctypes.c_int), ("scale_rule", ctypes.c_int)]
+                + [(n, ctypes.c_void_p) for n in ("global_scale", "codes", "scales", "d_status")])
 
 
 class _Weights(ctypes.Structure):
@@ -69,7 +97,7 @@ def lib():
                                "`python -m w4a16_matmul_pack_b200.build` (nvcc, sm_100a)")
         L = ctypes.CDLL(_LIB_PATH)
         P, I, U, S = ctypes.c_void_p, ctypes.c_int, ctypes.c_uint, ctypes.c_size_t
-        WP = ctypes.POINTER(_Weights)
+        WP, FP, LL = ctypes.POINTER(_Weights), ctypes.POINTER(_Fp4), ctypes.c_longlong
         sig = {
             "pack_nvfp4": ([P, I, I, I, I, P, P, P, P, S, P, P], I),
             "pack_nvfp4_ex": ([P, I, I, I, I, P, P, P, P, P, S, P, P], I),
@@ -87,6 +115,14 @@ def lib():
             "w4_encode_scalars": ([P, S, P, P, P], I),
             "w4_device_error": ([ctypes.POINTER(ctypes.c_int), I], I),
             "w4_set_wait_limit": ([ctypes.c_ulonglong], I),
+            "fp4_scale_bytes": ([I, I, I], S),
+            "fp4_quantize": ([P, I, LL, I, I, I, I, P, P, P, P, P], I),
+            "fp4_dequantize": ([FP, P, I, LL, P], I),
+            "fp4_tile_scales": ([I, I, I, P, P, P], I),
+            "w4a4_gemm": ([FP, FP, P, I, LL, U, P], I),
+            "w4a4_workspace_bytes": ([FP, I], S),
+            "w4a4_linear": ([FP, P, I, LL, I, I, P, P, I, LL, P, S, P, P], I),
+            "w4_block_norm": ([ctypes.POINTER(_Norm), P], I),
             "w4_status_string": ([I], ctypes.c_char_p),
             "w4_version": ([], ctypes.c_char_p),
         }
@@ -341,6 +377,315 @@ def w4a16_gemm(w: PackedWeights, x: torch.Tensor, *, want_f32: bool = True, want
     _check(lib().w4a16_gemm(ctypes.byref(s), _ptr(x), M, _ptr(out_f32), _ptr(out_bf16), _ptr(workspace),
                             0 if workspace is None else workspace.numel(), _stream(stream)), "w4a16_gemm")
     return out_f32, out_bf16
+
+
+# ------------------------------------------------------- 4-bit activations ----
+
+_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_FP4_FMTS = {"mxfp4": FMT_MXFP4, "nvfp4": FMT_NVFP4, FMT_MXFP4: FMT_MXFP4, FMT_NVFP4: FMT_NVFP4}
+_GATES = {"none": 0, "sigmoid": 1, "tanh": 2}
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _fp4_fmt(fmt) -> int:
+    if fmt not in _FP4_FMTS:
+        raise ValueError("fmt must be 'mxfp4' or 'nvfp4'")
+    return _FP4_FMTS[fmt]
+
+
+def _type(t: torch.Tensor, name: str) -> int:
+    if t.dtype not in _TYPES:
+        raise ValueError(f"{name} must be bfloat16, float16 or float32, got {t.dtype}")
+    return _TYPES[t.dtype]
+
+
+def _same_device(ref: torch.Tensor, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != ref.device:
+            raise ValueError(f"{name} must be on {ref.device}, got {t.device}")
+
+
+def _rows(t: torch.Tensor, name: str, shape=None):
+    """(data pointer, row distance) of a 2-D CUDA tensor whose rows are contiguous."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (no CPU path)")
+    if t.dim() != 2 or (shape is not None and tuple(t.shape) != shape):
+        raise ValueError(f"{name} must have shape {shape or '[rows][K]'}, got {tuple(t.shape)}")
+    rows, width = t.shape
+    if width > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return t.data_ptr(), t.stride(0) if rows > 1 else width
+
+
+def _scalar(t: Optional[torch.Tensor], name: str, dtype):
+    """Data pointer of an optional one-element CUDA tensor."""
+    if t is None:
+        return None
+    _cuda(t, name, dtype)
+    if t.numel() != 1:
+        raise ValueError(f"{name} must hold one value")
+    return t.data_ptr()
+
+
+def _call(device: torch.device, stream, what: str, fn, *args):
+    """fn(*args, stream) with `device` current; on its current stream when none is given."""
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _call(device, stream, what, fn, *args)
+    if stream is not None:
+        s = stream.cuda_stream
+    else:
+        s = _raw_stream(device.index) if _raw_stream else torch.cuda.current_stream(device).cuda_stream
+    status = fn(*args, s)
+    if status:
+        raise W4Error(status, what)
+
+
+@dataclass(frozen=True)
+class Fp4Tensor:
+    """A block-scaled 4-bit operand: rows x K values (w4_fp4 in include/w4a16.h).
+    Holds its tensors; the fields do not change after construction."""
+    fmt: int
+    rows: int
+    K: int
+    codes: torch.Tensor                    # uint8 [rows][K/2]
+    scales: torch.Tensor                   # uint8 [fp4_scale_bytes]: tiles of 128 rows x 4 scales
+    global_scale: Optional[torch.Tensor] = None   # float32 [1] (NVFP4)
+
+    def __post_init__(self):
+        _fp4_fmt(self.fmt)
+        _cuda(self.codes, "codes", torch.uint8)
+        _cuda(self.scales, "scales", torch.uint8)
+        if self.codes.numel() != self.rows * (self.K // 2):
+            raise ValueError("codes must hold rows * K / 2 bytes")
+        if self.scales.numel() != fp4_scale_bytes(self.fmt, self.rows, self.K):
+            raise ValueError("scales must hold fp4_scale_bytes(fmt, rows, K) bytes (K % 32 == 0)")
+        if (self.global_scale is None) != (self.fmt == FMT_MXFP4):
+            raise ValueError("global_scale goes with NVFP4")
+        g = _scalar(self.global_scale, "global_scale", torch.float32)
+        _same_device(self.codes, scales=self.scales, global_scale=self.global_scale)
+        c = _Fp4(self.fmt, self.rows, self.K, self.codes.data_ptr(), self.scales.data_ptr(), g)
+        object.__setattr__(self, "_c", c)
+        object.__setattr__(self, "_ref", ctypes.byref(c))
+
+    @property
+    def nbytes(self) -> int:
+        return self.codes.numel() + self.scales.numel()
+
+
+def fp4_scale_bytes(fmt: int, rows: int, K: int) -> int:
+    return lib().fp4_scale_bytes(fmt, rows, K)
+
+
+def _empty_fp4(fmt: int, rows: int, K: int, device, global_scale) -> Fp4Tensor:
+    if rows < 1 or K < 32 or K % 32:
+        raise W4Error(1, f"4-bit operand of {rows} x {K} (K % 32 == 0, one row at least)")
+    return Fp4Tensor(fmt, rows, K, torch.empty(rows, K // 2, dtype=torch.uint8, device=device),
+                     torch.empty(fp4_scale_bytes(fmt, rows, K), dtype=torch.uint8, device=device),
+                     global_scale if fmt == FMT_NVFP4 else None)
+
+
+def _check_out(out: Fp4Tensor, fmt: int, rows: int, K: int, global_scale):
+    if not isinstance(out, Fp4Tensor) or (out.fmt, out.rows, out.K) != (fmt, rows, K):
+        raise ValueError("out must be an Fp4Tensor of the result's format and shape")
+    if fmt == FMT_NVFP4 and global_scale is not None and out.global_scale.data_ptr() != global_scale.data_ptr():
+        raise ValueError("out.global_scale must be the given global_scale")
+    return out
+
+
+def fp4_quantize(x: torch.Tensor, fmt="mxfp4", *, global_scale: Optional[torch.Tensor] = None,
+                 scale_rule: int = MX_SCALE_FLOOR, out: Optional[Fp4Tensor] = None,
+                 d_status: Optional[torch.Tensor] = None, stream=None) -> Fp4Tensor:
+    """Quantise x[rows][K] (bf16, f16 or f32, K % 32 == 0) to "mxfp4" or, under a given
+    global_scale (float32 [1]), "nvfp4" (see fp4_quantize in include/w4a16.h)."""
+    fmt = _fp4_fmt(fmt)
+    ptr, ld = _rows(x, "x")
+    t = _type(x, "x")
+    rows, K = x.shape
+    g = _scalar(global_scale, "global_scale", torch.float32) if fmt == FMT_NVFP4 else None
+    if out is None:
+        if fmt == FMT_NVFP4 and g is None:
+            raise ValueError("nvfp4 needs a global_scale")
+        out = _empty_fp4(fmt, rows, K, x.device, global_scale)
+    else:
+        _check_out(out, fmt, rows, K, global_scale)
+    _same_device(x, out=out.codes, global_scale=out.global_scale, d_status=d_status)
+    c = out._c
+    _call(x.device, stream, "fp4_quantize", lib().fp4_quantize, ptr, t, ld, rows, K, fmt, scale_rule,
+          c.global_scale, c.codes, c.scales, _scalar(d_status, "d_status", torch.int32))
+    return out
+
+
+def fp4_dequantize(a: Fp4Tensor, dtype: torch.dtype = torch.bfloat16, *, out: Optional[torch.Tensor] = None,
+                   stream=None) -> torch.Tensor:
+    """The values [rows][K] an operand stands for (see fp4_dequantize in include/w4a16.h)."""
+    if out is None:
+        out = torch.empty(a.rows, a.K, dtype=dtype, device=a.codes.device)
+    ptr, ld = _rows(out, "out", (a.rows, a.K))
+    _same_device(a.codes, out=out)
+    _call(out.device, stream, "fp4_dequantize", lib().fp4_dequantize, a._ref, ptr, _type(out, "out"), ld)
+    return out
+
+
+def fp4_from_rows(fmt, codes: torch.Tensor, row_scales: torch.Tensor, global_scale: Optional[torch.Tensor] = None, *,
+                  stream=None) -> Fp4Tensor:
+    """An operand from codes [rows][K/2] (used as they are) and row-major scales
+    [rows][K/32] (MXFP4) or [rows][K/16] (NVFP4), which are laid out once."""
+    fmt = _fp4_fmt(fmt)
+    _cuda(codes, "codes", torch.uint8)
+    _cuda(row_scales, "row_scales", torch.uint8)
+    _same_device(codes, row_scales=row_scales, global_scale=global_scale)
+    if codes.dim() != 2:
+        raise ValueError("codes must have shape [rows][K/2]")
+    rows, K = codes.shape[0], 2 * codes.shape[1]
+    if tuple(row_scales.shape) != (rows, K // (32 if fmt == FMT_MXFP4 else 16)):
+        raise ValueError("row_scales do not match the codes")
+    if rows < 1 or K < 32 or K % 32:
+        raise W4Error(1, f"4-bit operand of {rows} x {K} (K % 32 == 0, one row at least)")
+    out = Fp4Tensor(fmt, rows, K, codes,
+                    torch.empty(fp4_scale_bytes(fmt, rows, K), dtype=torch.uint8, device=codes.device), global_scale)
+    _call(codes.device, stream, "fp4_tile_scales", lib().fp4_tile_scales, fmt, rows, K, row_scales.data_ptr(),
+          out._c.scales)
+    return out
+
+
+def fp4_from_packed(w: PackedWeights, *, stream=None) -> Fp4Tensor:
+    """NVFP4 weights from pack_nvfp4 as an operand of w4a4_gemm: codes and global
+    scale shared, scales laid out once."""
+    if w.fmt != FMT_NVFP4:
+        raise ValueError("only NVFP4 weights can be multiplied by 4-bit activations")
+    return fp4_from_rows(FMT_NVFP4, w.codes, w.scales, w.global_scale, stream=stream)
+
+
+def _product_out(w: Fp4Tensor, M: int, out_dtype, out: Optional[torch.Tensor], device):
+    if not isinstance(w, Fp4Tensor):
+        raise ValueError("w must be an Fp4Tensor (fp4_quantize, fp4_from_packed)")
+    if out is None:
+        out = torch.empty(M, w.rows, dtype=out_dtype, device=device)
+    ptr, ld = _rows(out, "out", (M, w.rows))
+    return out, ptr, ld, _type(out, "out")
+
+
+def w4a4_gemm(w: Fp4Tensor, x: Fp4Tensor, *, out_dtype: torch.dtype = torch.bfloat16,
+              out: Optional[torch.Tensor] = None, flags: int = 0, stream=None) -> torch.Tensor:
+    """y[M][N] = x_hat[M][K] . w_hat[N][K], both operands in 4 bits and of the same
+    format; any M (see w4a4_gemm in include/w4a16.h)."""
+    if not isinstance(x, Fp4Tensor):
+        raise ValueError("x must be an Fp4Tensor (fp4_quantize, block_norm)")
+    out, ptr, ld, t = _product_out(w, x.rows, out_dtype, out, x.codes.device)
+    _same_device(out, w=w.codes, x=x.codes)
+    _call(out.device, stream, "w4a4_gemm", lib().w4a4_gemm, w._ref, x._ref, ptr, t, ld, flags)
+    return out
+
+
+def w4a4_workspace_bytes(w: Fp4Tensor, M: int) -> int:
+    return lib().w4a4_workspace_bytes(w._ref, M)
+
+
+def w4a4_linear(w: Fp4Tensor, x: torch.Tensor, *, global_scale: Optional[torch.Tensor] = None,
+                scale_rule: int = MX_SCALE_FLOOR, out_dtype: torch.dtype = torch.bfloat16,
+                out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                d_status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """y[M][N] = quantised x[M][K] . w_hat: fp4_quantize to w's format (under
+    global_scale for NVFP4), then w4a4_gemm, in one call."""
+    ptr, ld = _rows(x, "x")
+    M, K = x.shape
+    out, yptr, yld, yt = _product_out(w, M, out_dtype, out, x.device)
+    if K != w.K:
+        raise ValueError(f"x has {K} columns, w {w.K}")
+    g = _scalar(global_scale, "global_scale", torch.float32) if w.fmt == FMT_NVFP4 else None
+    if workspace is None:
+        workspace = torch.empty(lib().w4a4_workspace_bytes(w._ref, M), dtype=torch.uint8, device=x.device)
+    else:
+        _cuda(workspace, "workspace", torch.uint8)
+    _same_device(x, w=w.codes, out=out, global_scale=global_scale, workspace=workspace, d_status=d_status)
+    _call(x.device, stream, "w4a4_linear", lib().w4a4_linear, w._ref, ptr, _type(x, "x"), ld, M, scale_rule, g,
+          yptr, yt, yld, workspace.data_ptr(), workspace.numel(), _scalar(d_status, "d_status", torch.int32))
+    return out
+
+
+def _width(t: Optional[torch.Tensor], name: str, D: int, dtype):
+    """Data pointer of an optional [D] tensor."""
+    if t is None:
+        return None
+    _cuda(t, name, dtype)
+    if tuple(t.shape) != (D,):
+        raise ValueError(f"{name} must have shape ({D},), got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def block_norm(y: torch.Tensor, h: Optional[torch.Tensor] = None, *, post_weight: Optional[torch.Tensor] = None,
+               pre_weight: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None, gate_act: str = "none",
+               gate_rows: Optional[int] = None, residual_scale: float = 1.0, block_scale: float = 1.0,
+               eps: float = 1e-6, weight_offset: float = 0.0, quantize=None,
+               global_scale: Optional[torch.Tensor] = None, scale_rule: int = MX_SCALE_FLOOR, want_h: bool = True,
+               out_h: Optional[torch.Tensor] = None, out=None, d_status: Optional[torch.Tensor] = None, stream=None):
+    """(h', z) between two blocks, for rows y[M][D], h[M][D] of one type (w4_block_norm
+    in include/w4a16.h):
+
+        b  = rmsnorm(y) * (post_weight + weight_offset)      (y itself without post_weight)
+        h' = residual_scale * h + block_scale * act(gate) * b
+        z  = rmsnorm(h') * (pre_weight + weight_offset)
+
+    gate: [D], or [G][D] where each row serves gate_rows consecutive rows of y (M / G
+    if not given); gate_act "none", "sigmoid" or "tanh".  quantize "mxfp4" or "nvfp4"
+    (under global_scale) gives z as an Fp4Tensor.  out_h may be h or y; want_h=False
+    leaves h' out (None)."""
+    yp, ldy = _rows(y, "y")
+    t = _type(y, "y")
+    M, D = y.shape
+    dev = y.device
+    n = _Norm(type=t, M=M, D=D, y=yp, ldy=ldy, residual_scale=residual_scale, block_scale=block_scale, eps=eps,
+              weight_offset=weight_offset, scale_rule=scale_rule,
+              w_post=_width(post_weight, "post_weight", D, y.dtype), w_pre=_width(pre_weight, "pre_weight", D, y.dtype))
+    if h is not None:
+        if h.dtype != y.dtype:
+            raise ValueError(f"h must be {y.dtype}, got {h.dtype}")
+        n.h, n.ldh = _rows(h, "h", (M, D))
+    if gate_act not in _GATES:
+        raise ValueError("gate_act must be 'none', 'sigmoid' or 'tanh'")
+    if gate is not None:
+        g2 = gate.unsqueeze(0) if gate.dim() == 1 else gate
+        if g2.dtype != y.dtype:
+            raise ValueError(f"gate must be {y.dtype}, got {g2.dtype}")
+        G = g2.shape[0]
+        if gate_rows is None:
+            if G < 1 or M % G:
+                raise ValueError(f"{G} gate rows do not divide {M} rows: give gate_rows")
+            gate_rows = M // G
+        if gate_rows < 1 or G * gate_rows < M:
+            raise ValueError(f"{G} gate rows of {gate_rows} rows each do not cover {M} rows")
+        n.gate, n.ldgate = _rows(g2, "gate", (G, D))
+        n.gate_rows, n.gate_act = min(gate_rows, M), _GATES[gate_act]
+    if out_h is None and want_h:
+        out_h = torch.empty(M, D, dtype=y.dtype, device=dev)
+    if out_h is not None:
+        if out_h.dtype != y.dtype:
+            raise ValueError(f"out_h must be {y.dtype}, got {out_h.dtype}")
+        n.h_out, n.ldh_out = _rows(out_h, "out_h", (M, D))
+    if quantize is None:
+        if out is None:
+            out = torch.empty(M, D, dtype=y.dtype, device=dev)
+        if out.dtype != y.dtype:
+            raise ValueError(f"out must be {y.dtype}, got {out.dtype}")
+        n.z, n.ldz = _rows(out, "out", (M, D))
+        zdev = out
+    else:
+        fmt = _fp4_fmt(quantize)
+        if out is None:
+            if fmt == FMT_NVFP4 and global_scale is None:
+                raise ValueError("nvfp4 needs a global_scale")
+            out = _empty_fp4(fmt, M, D, dev, global_scale)
+        else:
+            _check_out(out, fmt, M, D, global_scale)
+        c = out._c
+        n.quant_fmt, n.global_scale, n.codes, n.scales = fmt, c.global_scale, c.codes, c.scales
+        n.d_status = _scalar(d_status, "d_status", torch.int32)
+        zdev = out.codes
+    _same_device(y, h=h, gate=gate, post_weight=post_weight, pre_weight=pre_weight, out_h=out_h, out=zdev,
+                 global_scale=global_scale, d_status=d_status)
+    _call(dev, stream, "w4_block_norm", lib().w4_block_norm, ctypes.byref(n))
+    return out_h, out
 
 
 def w4_encode_scalars(v: torch.Tensor, stream=None):

@@ -12,7 +12,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 SRC_DIR = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libw4a16.so")
 MAIN = os.path.join(SRC_DIR, "w4a16.cu")
-UNITS = [MAIN, os.path.join(SRC_DIR, "noalloc.cu")]
+UNITS = [MAIN, os.path.join(SRC_DIR, "noalloc.cu"), os.path.join(SRC_DIR, "fp4.cu")]
 
 NVCC_FLAGS = [
     "-O3", "-std=c++17", "-lineinfo",
@@ -22,6 +22,7 @@ NVCC_FLAGS = [
     # IEEE binary32 division/sqrt and no flush-to-zero: the packer must take the
     # same rounding decisions as the specification.
     "-prec-div=true", "-prec-sqrt=true", "-ftz=false", "-fmad=true",
+    "--threads", "0",   # the translation units in parallel
 ]
 
 

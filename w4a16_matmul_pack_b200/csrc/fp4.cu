@@ -1,0 +1,366 @@
+// fp4.cu -- the W4A4 part of the C ABI (declared in include/w4a16.h): host-side
+// validation, launch configuration and launches of the sm_100a kernels that
+// quantise activations to 4 bits, multiply two 4-bit operands, and run the
+// norms, gate and residual between two such products.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "block_norm.cuh"
+#include "fp4.cuh"
+#include "fp4_gemm.cuh"
+
+using namespace w4;
+
+namespace w4 {
+
+// The sticky error word and the wait limit of this file's kernels are its own
+// copies (one per translation unit); w4_device_error and w4_set_wait_limit act on
+// both through these.
+int fp4_device_error(int *out, int clear) {
+    if (cudaMemcpyFromSymbol(out, g_device_error, sizeof(int)) != cudaSuccess) return W4_ERR_CUDA;
+    const int zero = 0;
+    if (clear && cudaMemcpyToSymbol(g_device_error, &zero, sizeof(int)) != cudaSuccess) return W4_ERR_CUDA;
+    return W4_OK;
+}
+
+int fp4_set_wait_limit(unsigned long long ns) {
+    return cudaMemcpyToSymbol(g_wait_limit_ns, &ns, sizeof(ns)) == cudaSuccess ? W4_OK : W4_ERR_CUDA;
+}
+
+}  // namespace w4
+
+namespace {
+
+inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+inline cudaStream_t as_stream(void *s) { return reinterpret_cast<cudaStream_t>(s); }
+inline w4_status launch_status() { return cudaGetLastError() == cudaSuccess ? W4_OK : W4_ERR_CUDA; }
+
+inline bool is_fp4(int fmt) { return fmt == W4_FMT_MXFP4 || fmt == W4_FMT_NVFP4; }
+inline int type_size(int type) { return type == W4_TYPE_F32 ? 4 : 2; }
+inline bool is_type(int type) { return type == W4_TYPE_BF16 || type == W4_TYPE_F16 || type == W4_TYPE_F32; }
+// Rows of `ld` values of `type` that all start on 16 bytes.
+inline bool rows16(long long ld, int type) { return ld * type_size(type) % 16 == 0; }
+
+constexpr long long kMaxBlocks = 0x7FFFFFFFll;
+
+w4_status device_sms(int &sms) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return W4_ERR_CUDA;
+    return W4_OK;
+}
+
+w4_status check_operand(const w4_fp4 *a) {
+    if (!a || !is_fp4(a->fmt) || a->rows < 1 || a->K < 32 || a->K % 32 || !a->codes || !a->scales) return W4_ERR_ARG;
+    if (a->fmt == W4_FMT_NVFP4 && !a->global_scale) return W4_ERR_ARG;
+    if (!aligned16(a->codes) || !aligned16(a->scales) || !aligned4(a->global_scale)) return W4_ERR_ALIGN;
+    return W4_OK;
+}
+
+// A quantiser's output side.
+w4_status check_quantised(int rows, int K, int fmt, int scale_rule, const float *global_scale, const uint8_t *codes,
+                          const uint8_t *scales, const int *d_status) {
+    if (!is_fp4(fmt) || rows < 1 || K < 32 || K % 32 || !codes || !scales) return W4_ERR_ARG;
+    if (scale_rule != W4_MX_SCALE_FLOOR && scale_rule != W4_MX_SCALE_CEIL) return W4_ERR_ARG;
+    if (fmt == W4_FMT_NVFP4 && (!global_scale || scale_rule != W4_MX_SCALE_FLOOR)) return W4_ERR_ARG;
+    if (!aligned16(codes) || !aligned16(scales) || !aligned4(global_scale) || !aligned4(d_status)) return W4_ERR_ALIGN;
+    return W4_OK;
+}
+
+fp4::Out quantised_out(int K, int fmt, int scale_rule, const float *global_scale, uint8_t *codes, uint8_t *scales,
+                       int *d_status) {
+    fp4::Out o;
+    o.codes = codes;
+    o.scales = scales;
+    o.global_scale = global_scale;
+    o.d_status = d_status;
+    o.K = K;
+    o.tiles_k = fp4::scale_tiles_k(fmt, K);
+    o.ceil_rule = scale_rule == W4_MX_SCALE_CEIL;
+    return o;
+}
+
+w4_status clear_status(int *d_status, cudaStream_t st) {
+    return !d_status || cudaMemsetAsync(d_status, 0, sizeof(int), st) == cudaSuccess ? W4_OK : W4_ERR_CUDA;
+}
+
+template <typename T>
+w4_status launch_quantize(const void *x, long long ldx, int rows, int fmt, const fp4::Out &o, cudaStream_t st) {
+    const int pieces = (o.K / fp4::kUnit + 31) / 32;
+    const long long blocks = ((long long)rows * pieces + 7) / 8;
+    if (blocks > kMaxBlocks) return W4_ERR_UNSUPPORTED;
+    if (fmt == W4_FMT_MXFP4)
+        fp4::quantize_kernel<T, W4_FMT_MXFP4>
+            <<<(unsigned)blocks, 256, 0, st>>>(reinterpret_cast<const T *>(x), ldx, rows, pieces, o);
+    else
+        fp4::quantize_kernel<T, W4_FMT_NVFP4>
+            <<<(unsigned)blocks, 256, 0, st>>>(reinterpret_cast<const T *>(x), ldx, rows, pieces, o);
+    return launch_status();
+}
+
+w4_status quantize(const void *x, int type, long long ldx, int rows, int fmt, const fp4::Out &o, cudaStream_t st) {
+    switch (type) {
+    case W4_TYPE_BF16: return launch_quantize<__nv_bfloat16>(x, ldx, rows, fmt, o, st);
+    case W4_TYPE_F16: return launch_quantize<__half>(x, ldx, rows, fmt, o, st);
+    case W4_TYPE_F32: return launch_quantize<float>(x, ldx, rows, fmt, o, st);
+    }
+    return W4_ERR_ARG;
+}
+
+template <typename T>
+w4_status launch_dequantize(const w4_fp4 *a, void *out, long long ldo, cudaStream_t st) {
+    const int pieces = (a->K / fp4::kUnit + 31) / 32, tiles_k = fp4::scale_tiles_k(a->fmt, a->K);
+    const long long blocks = ((long long)a->rows * pieces + 7) / 8;
+    if (blocks > kMaxBlocks) return W4_ERR_UNSUPPORTED;
+    if (a->fmt == W4_FMT_MXFP4)
+        fp4::dequantize_kernel<T, W4_FMT_MXFP4><<<(unsigned)blocks, 256, 0, st>>>(
+            a->codes, a->scales, a->global_scale, a->rows, a->K, tiles_k, pieces, reinterpret_cast<T *>(out), ldo);
+    else
+        fp4::dequantize_kernel<T, W4_FMT_NVFP4><<<(unsigned)blocks, 256, 0, st>>>(
+            a->codes, a->scales, a->global_scale, a->rows, a->K, tiles_k, pieces, reinterpret_cast<T *>(out), ldo);
+    return launch_status();
+}
+
+// ------------------------------------------------------------------ product --
+
+// Codes [rows][K/2] bytes as boxes of 128 bytes x `box_rows`, 128-byte swizzle;
+// bytes past a row's end and rows past the last arrive as zeros.
+bool codes_map(CUtensorMap &map, const uint8_t *codes, int rows, int K, int box_rows) {
+    PFN_encodeTiled enc = get_encode_tiled();
+    const cuuint64_t dims[2] = {(cuuint64_t)K / 2, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)K / 2};
+    const cuuint32_t box[2] = {fgemm::BK / 2, (cuuint32_t)box_rows};
+    const cuuint32_t estr[2] = {1, 1};
+    return enc && enc(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(codes), dims, strides, box, estr,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int FMT, int NT, bool SWAP>
+w4_status launch_gemm(const w4_fp4 *a, const w4_fp4 *b, void *y, long long ldy, int out_type, bool early_w,
+                      cudaStream_t st) {
+    using namespace fgemm;
+    CUtensorMap amap, bmap;
+    if (!codes_map(amap, a->codes, a->rows, a->K, BM) || !codes_map(bmap, b->codes, b->rows, b->K, NT))
+        return W4_ERR_CUDA;
+    int sms = 0;
+    if (device_sms(sms) != W4_OK) return W4_ERR_CUDA;
+    constexpr size_t smem = sizeof(Shared<FMT, NT>) + 1024;
+    static_assert(smem <= 227 * 1024, "shared memory of the product");
+    auto kernel = gemm_kernel<FMT, NT, SWAP>;
+    if (!set_smem_limit(reinterpret_cast<const void *>(kernel), smem)) return W4_ERR_CUDA;
+    Params p;
+    p.sfa = a->scales;
+    p.sfb = b->scales;
+    p.ga = FMT == W4_FMT_NVFP4 ? a->global_scale : nullptr;
+    p.gb = FMT == W4_FMT_NVFP4 ? b->global_scale : nullptr;
+    p.y = y;
+    p.ldy = ldy;
+    p.rows_a = a->rows;
+    p.rows_b = b->rows;
+    p.K = a->K;
+    p.tiles_a = (a->rows + BM - 1) / BM;
+    p.tiles_b = (b->rows + NT - 1) / NT;
+    p.tiles_k = fp4::scale_tiles_k(FMT, a->K);
+    p.out_type = out_type;
+    p.early_w = early_w;
+    const long long ntiles = (long long)p.tiles_a * p.tiles_b;
+    if (ntiles > kMaxBlocks) return W4_ERR_UNSUPPORTED;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)std::min<long long>(ntiles, sms), 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    // The kernel waits for the previous one on the stream before it reads or
+    // writes global memory; only its prologue overlaps that kernel's tail.
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kernel, amap, bmap, p) != cudaSuccess) return W4_ERR_CUDA;
+    return launch_status();
+}
+
+template <int FMT>
+w4_status gemm_fmt(const w4_fp4 *w, const w4_fp4 *x, void *y, long long ldy, int out_type, bool early_w,
+                   cudaStream_t st) {
+    const int M = x->rows;
+    if (M <= 16) return launch_gemm<FMT, 16, true>(w, x, y, ldy, out_type, early_w, st);
+    if (M <= 64) return launch_gemm<FMT, 64, true>(w, x, y, ldy, out_type, early_w, st);
+    return launch_gemm<FMT, 128, false>(x, w, y, ldy, out_type, early_w, st);
+}
+
+w4_status check_product(const w4_fp4 *w, const w4_fp4 *x, const void *y, long long ldy, int out_type) {
+    w4_status s = check_operand(w);
+    if (s != W4_OK) return s;
+    if ((s = check_operand(x)) != W4_OK) return s;
+    if (w->fmt != x->fmt || w->K != x->K || !y || !is_type(out_type) || ldy < w->rows) return W4_ERR_ARG;
+    if (!aligned16(y)) return W4_ERR_ALIGN;
+    return W4_OK;
+}
+
+w4_status product(const w4_fp4 *w, const w4_fp4 *x, void *y, long long ldy, int out_type, bool early_w,
+                  cudaStream_t st) {
+    return w->fmt == W4_FMT_MXFP4 ? gemm_fmt<W4_FMT_MXFP4>(w, x, y, ldy, out_type, early_w, st)
+                                  : gemm_fmt<W4_FMT_NVFP4>(w, x, y, ldy, out_type, early_w, st);
+}
+
+// Codes first, then scales on the next 256 bytes.
+size_t linear_scales_at(int rows, int K) { return ((size_t)rows * (K / 2) + 255) & ~(size_t)255; }
+
+// -------------------------------------------------------------------- norms --
+
+template <typename T, int PV, int MAXT, int QFMT>
+void launch_norm_mode(const norm::Args &a, int mode, int M, int threads, cudaStream_t st) {
+    if (mode == norm::VECTOR)
+        norm::block_norm_kernel<T, PV, MAXT, norm::VECTOR, QFMT><<<M, threads, 0, st>>>(a);
+    else if constexpr (QFMT != 0)
+        norm::block_norm_kernel<T, PV, MAXT, norm::SCALAR, QFMT><<<M, threads, 0, st>>>(a);
+    else
+        norm::block_norm_kernel<T, PV, MAXT, norm::STRIDED, QFMT><<<M, threads, 0, st>>>(a);
+}
+
+template <typename T, int QFMT>
+w4_status launch_norm(const norm::Args &a, int mode, int M, cudaStream_t st) {
+    const int units = (a.D + fp4::kUnit - 1) / fp4::kUnit;
+    auto threads = [&](int pv) { return ((units + pv - 1) / pv + 31) / 32 * 32; };
+    if (units <= 512) launch_norm_mode<T, 1, 512, QFMT>(a, mode, M, threads(1), st);
+    else if (units <= 1024) launch_norm_mode<T, 2, 512, QFMT>(a, mode, M, threads(2), st);
+    else if (units <= 2048) launch_norm_mode<T, 4, 512, QFMT>(a, mode, M, threads(4), st);
+    else launch_norm_mode<T, 4, 1024, QFMT>(a, mode, M, threads(4), st);
+    return launch_status();
+}
+
+template <typename T>
+w4_status launch_norm_fmt(const norm::Args &a, int mode, int M, int fmt, cudaStream_t st) {
+    if (fmt == 0) return launch_norm<T, 0>(a, mode, M, st);
+    if (fmt == W4_FMT_MXFP4) return launch_norm<T, W4_FMT_MXFP4>(a, mode, M, st);
+    return launch_norm<T, W4_FMT_NVFP4>(a, mode, M, st);
+}
+
+}  // namespace
+
+// ======================================================================== ABI
+
+extern "C" {
+
+size_t fp4_scale_bytes(int fmt, int rows, int K) {
+    if (!is_fp4(fmt) || rows < 1 || K < 32 || K % 32) return 0;
+    return ((size_t)rows + 127) / 128 * fp4::scale_tiles_k(fmt, K) * 512;
+}
+
+w4_status fp4_quantize(const void *x, int type, long long ldx, int rows, int K, int fmt, int scale_rule,
+                       const float *global_scale, uint8_t *codes, uint8_t *scales, int *d_status, void *stream) {
+    w4_status s = check_quantised(rows, K, fmt, scale_rule, global_scale, codes, scales, d_status);
+    if (s != W4_OK) return s;
+    if (!x || !is_type(type) || ldx < K) return W4_ERR_ARG;
+    if (!aligned16(x) || !rows16(ldx, type)) return W4_ERR_ALIGN;
+    cudaStream_t st = as_stream(stream);
+    if (clear_status(d_status, st) != W4_OK) return W4_ERR_CUDA;
+    return quantize(x, type, ldx, rows, fmt, quantised_out(K, fmt, scale_rule, global_scale, codes, scales, d_status),
+                    st);
+}
+
+w4_status fp4_dequantize(const w4_fp4 *a, void *out, int type, long long ldo, void *stream) {
+    const w4_status s = check_operand(a);
+    if (s != W4_OK) return s;
+    if (!out || !is_type(type) || ldo < a->K) return W4_ERR_ARG;
+    if (!aligned16(out) || !rows16(ldo, type)) return W4_ERR_ALIGN;
+    cudaStream_t st = as_stream(stream);
+    if (type == W4_TYPE_BF16) return launch_dequantize<__nv_bfloat16>(a, out, ldo, st);
+    if (type == W4_TYPE_F16) return launch_dequantize<__half>(a, out, ldo, st);
+    return launch_dequantize<float>(a, out, ldo, st);
+}
+
+w4_status fp4_tile_scales(int fmt, int rows, int K, const uint8_t *row_scales, uint8_t *scales, void *stream) {
+    if (!is_fp4(fmt) || rows < 1 || K < 32 || K % 32 || !row_scales || !scales) return W4_ERR_ARG;
+    if (!aligned16(row_scales) || !aligned16(scales)) return W4_ERR_ALIGN;
+    const int tiles_k = fp4::scale_tiles_k(fmt, K);
+    const long long blocks = ((long long)rows * tiles_k + 255) / 256;
+    if (blocks > kMaxBlocks) return W4_ERR_UNSUPPORTED;
+    fp4::tile_scales_kernel<<<(unsigned)blocks, 256, 0, as_stream(stream)>>>(
+        row_scales, rows, K / (fmt == W4_FMT_MXFP4 ? 32 : 16), tiles_k, scales);
+    return launch_status();
+}
+
+w4_status w4a4_gemm(const w4_fp4 *w, const w4_fp4 *x, void *y, int out_type, long long ldy, unsigned flags,
+                    void *stream) {
+    const w4_status s = check_product(w, x, y, ldy, out_type);
+    if (s != W4_OK) return s;
+    if (flags & ~W4_LAUNCH_PDL) return W4_ERR_ARG;
+    return product(w, x, y, ldy, out_type, (flags & W4_LAUNCH_PDL) != 0, as_stream(stream));
+}
+
+size_t w4a4_workspace_bytes(const w4_fp4 *w, int M) {
+    if (check_operand(w) != W4_OK || M < 1) return 0;
+    return linear_scales_at(M, w->K) + fp4_scale_bytes(w->fmt, M, w->K);
+}
+
+w4_status w4a4_linear(const w4_fp4 *w, const void *x, int type, long long ldx, int M, int scale_rule,
+                      const float *global_scale, void *y, int out_type, long long ldy, void *workspace,
+                      size_t workspace_bytes, int *d_status, void *stream) {
+    w4_status s = check_operand(w);
+    if (s != W4_OK) return s;
+    if (M < 1 || !x || !is_type(type) || ldx < w->K) return W4_ERR_ARG;
+    if (!workspace || workspace_bytes < w4a4_workspace_bytes(w, M)) return W4_ERR_WORKSPACE;
+    uint8_t *codes = reinterpret_cast<uint8_t *>(workspace), *scales = codes + linear_scales_at(M, w->K);
+    const w4_fp4 q = {w->fmt, M, w->K, codes, scales, global_scale};
+    if ((s = check_quantised(M, w->K, w->fmt, scale_rule, global_scale, codes, scales, d_status)) != W4_OK) return s;
+    if ((s = check_product(w, &q, y, ldy, out_type)) != W4_OK) return s;
+    if (!aligned16(x) || !rows16(ldx, type)) return W4_ERR_ALIGN;
+    cudaStream_t st = as_stream(stream);
+    if (clear_status(d_status, st) != W4_OK) return W4_ERR_CUDA;
+    s = quantize(x, type, ldx, M, w->fmt,
+                 quantised_out(w->K, w->fmt, scale_rule, global_scale, codes, scales, d_status), st);
+    if (s != W4_OK) return s;
+    // the kernel just launched does not write the weights
+    return product(w, &q, y, ldy, out_type, true, st);
+}
+
+w4_status w4_block_norm(const w4_norm *n, void *stream) {
+    if (!n || !n->y || n->M < 1 || n->D < 1 || !is_type(n->type) || !(n->eps >= 0.0f)) return W4_ERR_ARG;
+    if (n->D > norm::kMaxD) return W4_ERR_UNSUPPORTED;
+    if (n->ldy < n->D || (n->h && n->ldh < n->D) || (n->h_out && n->ldh_out < n->D)) return W4_ERR_ARG;
+    if (n->gate && (n->gate_rows < 1 || n->ldgate < n->D)) return W4_ERR_ARG;
+    if (n->gate_act < W4_GATE_NONE || n->gate_act > W4_GATE_TANH) return W4_ERR_ARG;
+    const int size = type_size(n->type);
+    auto on = [&](const void *p, int bytes) { return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(bytes - 1)) == 0; };
+    const void *ptrs[] = {n->y, n->h, n->w_post, n->w_pre, n->gate, n->h_out, n->z};
+    bool vec = n->D % fp4::kUnit == 0 && rows16(n->ldy, n->type) && (!n->h || rows16(n->ldh, n->type)) &&
+               (!n->h_out || rows16(n->ldh_out, n->type)) && (!n->gate || rows16(n->ldgate, n->type));
+    for (const void *q : ptrs) {
+        if (!on(q, size)) return W4_ERR_ALIGN;
+        vec = vec && on(q, 16);
+    }
+    norm::Args a = {};
+    if (n->quant_fmt) {
+        const w4_status s = check_quantised(n->M, n->D, n->quant_fmt, n->scale_rule, n->global_scale, n->codes,
+                                            n->scales, n->d_status);
+        if (s != W4_OK) return s;
+        if (n->z) return W4_ERR_ARG;
+        a.q = quantised_out(n->D, n->quant_fmt, n->scale_rule, n->global_scale, n->codes, n->scales, n->d_status);
+    } else {
+        if (!n->z || n->ldz < n->D) return W4_ERR_ARG;
+        vec = vec && rows16(n->ldz, n->type);
+    }
+    a.y = n->y, a.h = n->h, a.w_post = n->w_post, a.w_pre = n->w_pre, a.gate = n->gate;
+    a.h_out = n->h_out, a.z = n->z;
+    a.ldy = n->ldy, a.ldh = n->ldh, a.ldgate = n->ldgate, a.ldh_out = n->ldh_out, a.ldz = n->ldz;
+    a.D = n->D, a.gate_rows = n->gate_rows, a.gate_act = n->gate_act;
+    a.residual_scale = n->residual_scale, a.block_scale = n->block_scale, a.eps = n->eps, a.offset = n->weight_offset;
+    cudaStream_t st = as_stream(stream);
+    if (n->quant_fmt && clear_status(n->d_status, st) != W4_OK) return W4_ERR_CUDA;
+    const int mode = vec ? norm::VECTOR : n->quant_fmt ? norm::SCALAR : norm::STRIDED;
+    switch (n->type) {
+    case W4_TYPE_BF16: return launch_norm_fmt<__nv_bfloat16>(a, mode, n->M, n->quant_fmt, st);
+    case W4_TYPE_F16: return launch_norm_fmt<__half>(a, mode, n->M, n->quant_fmt, st);
+    case W4_TYPE_F32: return launch_norm_fmt<float>(a, mode, n->M, n->quant_fmt, st);
+    }
+    return W4_ERR_ARG;
+}
+
+}  // extern "C"

@@ -15,6 +15,12 @@
 
 using namespace w4;
 
+namespace w4 {
+// The error word and the wait limit of the kernels in fp4.cu.
+int fp4_device_error(int *out, int clear);
+int fp4_set_wait_limit(unsigned long long ns);
+}  // namespace w4
+
 namespace {
 
 constexpr int kMaxDevices = 64;
@@ -694,6 +700,9 @@ w4_status w4_device_error(int *out, int clear) {
         const int zero = 0;
         if (cudaMemcpyToSymbol(g_device_error, &zero, sizeof(int)) != cudaSuccess) return W4_ERR_CUDA;
     }
+    int fp4 = 0;
+    if (fp4_device_error(&fp4, clear) != W4_OK) return W4_ERR_CUDA;
+    if (*out == 0) *out = fp4;
     return W4_OK;
 }
 
@@ -714,7 +723,7 @@ const char *w4_status_string(int status) {
 w4_status w4_set_wait_limit(unsigned long long ns) {
     const unsigned long long v = ns ? ns : kWaitLimitNs;
     if (cudaMemcpyToSymbol(g_wait_limit_ns, &v, sizeof(v)) != cudaSuccess) return W4_ERR_CUDA;
-    return W4_OK;
+    return fp4_set_wait_limit(v) == W4_OK ? W4_OK : W4_ERR_CUDA;
 }
 
 const char *w4_version(void) { return "w4a16 0.2.0 (sm_100a)"; }
