@@ -4,11 +4,14 @@
 // norms, gate and residual between two such products.
 #include <cuda_runtime.h>
 
+#include <stdlib.h>
+
 #include <algorithm>
 
 #include "block_norm.cuh"
 #include "fp4.cuh"
 #include "fp4_gemm.cuh"
+#include "fp4_skinny.cuh"
 
 using namespace w4;
 
@@ -140,9 +143,10 @@ bool codes_map(CUtensorMap &map, const uint8_t *codes, int rows, int K, int box_
 }
 
 template <int FMT, int NT, bool SWAP>
-w4_status launch_gemm(const w4_fp4 *a, const w4_fp4 *b, void *y, long long ldy, int out_type, bool early_w,
+w4_status launch_skinny(const w4_fp4 *a, const w4_fp4 *b, void *y, long long ldy, int out_type, bool early_w,
                       cudaStream_t st) {
     using namespace fgemm;
+    using namespace fgemm::skinny;
     CUtensorMap amap, bmap;
     if (!codes_map(amap, a->codes, a->rows, a->K, BM) || !codes_map(bmap, b->codes, b->rows, b->K, NT))
         return W4_ERR_CUDA;
@@ -185,13 +189,85 @@ w4_status launch_gemm(const w4_fp4 *a, const w4_fp4 *b, void *y, long long ldy, 
     return launch_status();
 }
 
+// Scale tiles as rows of 128 words, boxes of `tiles` rows; past the last row zeros.
+bool scales_map(CUtensorMap &map, const uint8_t *scales, size_t bytes, int tiles) {
+    PFN_encodeTiled enc = get_encode_tiled();
+    const cuuint64_t dims[2] = {fgemm::SF_TILE / 4, (cuuint64_t)(bytes / fgemm::SF_TILE)};
+    const cuuint64_t strides[1] = {fgemm::SF_TILE};
+    const cuuint32_t box[2] = {fgemm::SF_TILE / 4, (cuuint32_t)tiles};
+    const cuuint32_t estr[2] = {1, 1};
+    return enc && enc(&map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<uint8_t *>(scales), dims, strides, box, estr,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Bytes of the widest store that every output row is aligned for.
+int store_bytes(const void *y, long long ldy, int type) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(y) | (uintptr_t)(ldy * type_size(type));
+    return a % 32 == 0 ? 32 : a % 16 == 0 ? 16 : 0;
+}
+
+template <int FMT, int NT>
+w4_status launch_pair(const w4_fp4 *w, const w4_fp4 *x, void *y, long long ldy, int out_type, cudaStream_t st) {
+    using namespace fgemm;
+    using namespace fgemm::pair;
+    CUtensorMap xmap, wmap, sxmap, swmap;
+    constexpr int ST = Scales<FMT>::TILES;
+    if (!codes_map(xmap, x->codes, x->rows, x->K, BM) || !codes_map(wmap, w->codes, w->rows, w->K, NT / 2) ||
+        !scales_map(sxmap, x->scales, fp4_scale_bytes(FMT, x->rows, x->K), ST) ||
+        !scales_map(swmap, w->scales, fp4_scale_bytes(FMT, w->rows, w->K), ST))
+        return W4_ERR_CUDA;
+    int sms = 0;
+    if (device_sms(sms) != W4_OK) return W4_ERR_CUDA;
+    constexpr size_t smem = sizeof(pair::Shared<FMT, NT>) + 1024;
+    static_assert(smem <= 227 * 1024, "shared memory of the product");
+    auto kernel = pair::gemm_kernel<FMT, NT>;
+    if (!set_smem_limit(reinterpret_cast<const void *>(kernel), smem)) return W4_ERR_CUDA;
+    pair::Params p;
+    p.gx = FMT == W4_FMT_NVFP4 ? x->global_scale : nullptr;
+    p.gw = FMT == W4_FMT_NVFP4 ? w->global_scale : nullptr;
+    p.y = y;
+    p.ldy = ldy;
+    p.M = x->rows;
+    p.N = w->rows;
+    p.K = x->K;
+    p.tiles_m = (x->rows + 2 * BM - 1) / (2 * BM);
+    p.tiles_n = (w->rows + NT - 1) / NT;
+    p.tiles_k = fp4::scale_tiles_k(FMT, x->K);
+    p.out_type = out_type;
+    p.vec = store_bytes(y, ldy, out_type);
+    const long long ntiles = (long long)p.tiles_m * p.tiles_n;
+    if (ntiles > kMaxBlocks) return W4_ERR_UNSUPPORTED;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * (unsigned)std::min<long long>(ntiles, std::max(1, sms / 2)), 1, 1);
+    cfg.blockDim = dim3(pair::kThreads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    if (cudaLaunchKernelEx(&cfg, kernel, xmap, wmap, sxmap, swmap, p) != cudaSuccess) return W4_ERR_CUDA;
+    return launch_status();
+}
+
 template <int FMT>
 w4_status gemm_fmt(const w4_fp4 *w, const w4_fp4 *x, void *y, long long ldy, int out_type, bool early_w,
                    cudaStream_t st) {
     const int M = x->rows;
-    if (M <= 16) return launch_gemm<FMT, 16, true>(w, x, y, ldy, out_type, early_w, st);
-    if (M <= 64) return launch_gemm<FMT, 64, true>(w, x, y, ldy, out_type, early_w, st);
-    return launch_gemm<FMT, 128, false>(x, w, y, ldy, out_type, early_w, st);
+    if (M <= 16) return launch_skinny<FMT, 16, true>(w, x, y, ldy, out_type, early_w, st);
+    if (M <= 64) return launch_skinny<FMT, 64, true>(w, x, y, ldy, out_type, early_w, st);
+    if (M <= 128) return launch_skinny<FMT, 128, true>(w, x, y, ldy, out_type, early_w, st);
+    const char *e = getenv("W4_NT");
+    const int nt = e ? atoi(e) : 256;
+    if (nt == 192) return launch_pair<FMT, 192>(w, x, y, ldy, out_type, st);
+    if (nt == 128) return launch_pair<FMT, 128>(w, x, y, ldy, out_type, st);
+    return launch_pair<FMT, 256>(w, x, y, ldy, out_type, st);
 }
 
 w4_status check_product(const w4_fp4 *w, const w4_fp4 *x, const void *y, long long ldy, int out_type) {

@@ -1,186 +1,139 @@
-// fp4_gemm.cuh -- W4A4 product on the 5th-generation tensor cores (sm_100a):
+// fp4_gemm.cuh -- W4A4 product for prompts on the 5th-generation tensor cores
+// (sm_100a):
 //   y[m][n] = gx * gw * sum_k (x[m][k] * sx[m][k / B]) * (w[n][k] * sw[n][k / B])
 // with both operands block-scaled E2M1 (fp4.cuh): tcgen05.mma kind::mxf4 (MXFP4,
 // B = 32, E8M0) or kind::mxf4nvf4 (NVFP4, B = 16, E4M3).  The tensor cores apply
-// the block scales, so nothing is decoded: codes go from global to shared memory
-// by TMA, scale tiles (512 bytes, 128 rows x 4 scales) by bulk copies and from
-// there to tensor memory by tcgen05.cp; accumulators are binary32 in tensor
-// memory.  gx * gw is applied in the epilogue.
+// the block scales, so nothing is decoded: codes and scale tiles go from global to
+// shared memory by TMA, scales from there to tensor memory by tcgen05.cp;
+// accumulators are binary32 in tensor memory.  gx * gw is applied in the epilogue.
 //
-// Tile: 128 rows of the operand A (tensor-memory lanes) x NT rows of B x 256 k
-// per stage.  SWAP = false (prompts): A is x, so a thread of the epilogue holds
-// part of an output row.  SWAP = true (few tokens): A is w, so that 128 x NT
-// wastes no work on missing tokens; lanes then run along n.
+// A cluster of two CTAs works on one tile of 256 tokens x NT weight rows
+// (cta_group::2): each CTA stages its 128 tokens and half of the weight rows, and
+// holds its 128 tokens' accumulators.  One CTA alone would have to write and read
+// 12 KB of shared memory per 128-cycle MMA step (128 x 256 x 64), above the 128
+// bytes per cycle the memory gives; the pair moves 8 KB per CTA and step.
 //
-// Warp roles (6 warps): 0 TMA producer; 1 tensor-memory allocation, scale copies
-// and MMAs (one lane); 2-5 epilogue (warp w reads lanes 32 (w % 4) .. + 31).
-// Persistent CTAs, one per SM; two accumulators, so the epilogue of a tile
-// overlaps the next tile's MMAs.  Every mbarrier wait is bounded (common.cuh).
+// Tensor memory: two accumulators of NT columns and the scales of one stage (the
+// MMAs and scale copies of one thread run in order).  At NT = 256 two accumulators
+// and the scales do not fit, so they share the middle columns: the epilogue
+// drains those first, and the next tile's MMAs start when they are free.
+//
+// Warp roles (10 warps, both CTAs unless said): 0 TMA producer; 1 tensor-memory
+// allocation, scale copies and MMAs (one lane of the first CTA); 2-9 epilogue (warp
+// w reads lanes 32 (w % 4) .. + 31, every second chunk of 32 columns).  Every
+// mbarrier wait is bounded (fp4_mma.cuh).
 #pragma once
 
-#include "fp4.cuh"
+#include "fp4_mma.cuh"
 
 namespace w4 {
 
 namespace fgemm {
 
-constexpr int BM = 128;
-constexpr int BK = 256;                 // k per stage: one 128-byte swizzle row of codes
-constexpr int STAGES = 4;
-constexpr int kWarps = 6;
+namespace pair {
+
+constexpr int kEpiWarps = 8;
+constexpr int kEpiWarp0 = 2;
+constexpr int kWarps = kEpiWarp0 + kEpiWarps;
 constexpr int kThreads = kWarps * 32;
-constexpr int kEpiWarps = 4;
-constexpr uint32_t A_BYTES = BM * (BK / 2);
-
-enum { OUT_BF16 = W4_TYPE_BF16, OUT_F16 = W4_TYPE_F16, OUT_F32 = W4_TYPE_F32 };
-
-template <int FMT> struct Scales;
-// TILES scale tiles along K per stage; STEP_TILES(j): the tile of MMA step j (64 k)
-template <> struct Scales<W4_FMT_MXFP4> { static constexpr int TILES = 2, STEPS_PER_TILE = 2; };
-template <> struct Scales<W4_FMT_NVFP4> { static constexpr int TILES = 4, STEPS_PER_TILE = 1; };
-
-constexpr uint32_t pow2_at_least(uint32_t v) {
-    uint32_t p = 32;
-    while (p < v) p *= 2;
-    return p;
-}
+constexpr int CHUNK = 32;                // accumulator columns per epilogue step
+constexpr uint32_t kSmemBudget = 224 * 1024;
 
 template <int FMT, int NT>
 struct Config {
     static constexpr int ST = Scales<FMT>::TILES;
-    static constexpr int GB = (NT + 127) / 128;                 // 128-row groups of a B tile
-    static constexpr uint32_t B_BYTES = NT * (BK / 2);
-    static constexpr uint32_t SF_TILE = 512;
-    static constexpr uint32_t SF_COLS = 4 * ST * (1 + GB);      // tensor-memory columns of a stage's scales
-    static constexpr uint32_t ACC_COLS = NT < 32 ? 32 : NT;
-    static constexpr uint32_t SF_COL0 = 2 * ACC_COLS;
-    static constexpr uint32_t TMEM_COLS = pow2_at_least(SF_COL0 + STAGES * SF_COLS);
-    static_assert(TMEM_COLS <= 512, "tensor memory");
-    // Instruction descriptor: A and B E2M1 (bits 7-9, 10-11), N >> 3 at bit 17,
-    // scale type at bit 23 (1: E8M0, 0: E4M3), M >> 7 at bit 27, both K-major.
-    // The scale ids (bits 4-5 of B, 29-30 of A) select the bytes of a scale word.
-    static constexpr uint32_t IDESC = (1u << 7) | (1u << 10) | ((uint32_t)(NT >> 3) << 17) |
-                                      ((FMT == W4_FMT_MXFP4 ? 1u : 0u) << 23) | ((uint32_t)(BM >> 7) << 27);
+    // 128-row scale groups a tile of NT rows touches.  NT is a multiple of 64: a tile
+    // starts on column 0 or 2 of its first group's scales (an MMA's scale address must
+    // be a multiple of two columns).
+    static constexpr int GB = (NT + 64) / 128;
+    static constexpr uint32_t B_BYTES = NT / 2 * (BK / 2);
+    static constexpr uint32_t SF_BYTES = SF_TILE * ST;                      // one group, one stage
+    static constexpr uint32_t STAGE_BYTES = A_BYTES + B_BYTES + (1 + GB) * SF_BYTES;   // of one CTA
+    static constexpr int STAGES = (int)(kSmemBudget / STAGE_BYTES) < 8 ? (int)(kSmemBudget / STAGE_BYTES) : 8;
+    static constexpr uint32_t SF_COLS = 4 * ST * (1 + GB);
+    static constexpr uint32_t SF_COL0 = 512 - SF_COLS;
+    static constexpr uint32_t ACC1 = NT < SF_COL0 - NT ? NT : SF_COL0 - NT;  // first column of accumulator 1
+    static constexpr int OVERLAP = NT - (int)ACC1;                           // columns the accumulators share
+    static constexpr int OVERLAP_CHUNKS = (OVERLAP + CHUNK - 1) / CHUNK;
+    static_assert(NT % 64 == 0 && NT <= 256 && STAGES >= 3 && OVERLAP <= 2 * CHUNK, "tile");
 };
 
 template <int FMT, int NT>
 struct Shared {
     using C = Config<FMT, NT>;
-    uint8_t a[STAGES][A_BYTES];                              // 1024-byte aligned (swizzle atoms)
-    uint8_t b[STAGES][C::B_BYTES];
-    uint8_t sfa[STAGES][C::ST][C::SF_TILE];
-    uint8_t sfb[STAGES][C::ST][C::GB][C::SF_TILE];
-    uint64_t full[STAGES], empty[STAGES];
-    uint64_t acc_full[2], acc_empty[2];
+    uint8_t a[C::STAGES][A_BYTES];                 // 1024-byte aligned (swizzle atoms)
+    uint8_t b[C::STAGES][C::B_BYTES];
+    uint8_t sfa[C::STAGES][C::ST][SF_TILE];
+    uint8_t sfb[C::STAGES][C::GB][C::ST][SF_TILE];
+    uint64_t full[C::STAGES], empty[C::STAGES];    // full: the first CTA's, for both CTAs' loads
+    uint64_t acc_full[2], acc_empty[2];            // acc_empty: the first CTA's, for both CTAs' epilogues
     uint64_t mma_done;
     uint32_t tmem_base;
     int abort;
 };
 
 struct Params {
-    const uint8_t *sfa, *sfb;      // scale tiles of A and B
-    const float *ga, *gb;          // global scales (NVFP4) or null
+    const float *gx, *gw;          // global scales (NVFP4) or null
     void *y;
     long long ldy;
-    int rows_a, rows_b, K;
-    int tiles_a, tiles_b, tiles_k; // tiles_k: scale tiles along K
+    int M, N, K;
+    int tiles_m, tiles_n, tiles_k; // tiles_k: scale tiles along K
     int out_type;
-    int early_w;                   // the weights may be read before the previous kernel has completed
+    int vec;                       // bytes of the widest aligned store: 32, 16 or 0 (single values)
 };
 
-__device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
-    uint64_t d = (uint64_t)((saddr & 0x3FFFFu) >> 4);
-    d |= (uint64_t)1 << 16;            // leading byte offset (unused for this layout)
-    d |= (uint64_t)(1024 >> 4) << 32;  // stride byte offset: 8-row atoms
-    d |= (uint64_t)1 << 46;            // version
-    d |= (uint64_t)2 << 61;            // SWIZZLE_128B
-    return d;
+// Arrives on the barrier at this offset in both CTAs once the MMAs and copies
+// issued so far have completed.
+__device__ __forceinline__ void commit_pair(uint64_t *bar) {
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+                 ::"r"(smem_addr(bar)), "h"((uint16_t)3) : "memory");
 }
 
-// A scale tile: 32 rows of 16 bytes, no swizzle, 8-row groups 128 bytes apart.
-__device__ __forceinline__ uint64_t scale_desc(uint32_t saddr) {
-    uint64_t d = (uint64_t)((saddr & 0x3FFFFu) >> 4);
-    d |= (uint64_t)(128 >> 4) << 16;
-    d |= (uint64_t)(128 >> 4) << 32;
-    d |= (uint64_t)1 << 46;
-    return d;
+// 2-D TMA load into this CTA's shared memory, bytes counted on a barrier of either CTA of the pair.
+__device__ __forceinline__ void tma_load_pair(void *dst, const CUtensorMap *map, int c0, int c1, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
+        "[%0], [%1, {%2, %3}], [%4];"
+        ::"r"(smem_addr(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar) : "memory");
 }
 
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-
-__device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t desc) {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+// This shared-memory address in the first CTA of the cluster.
+__device__ __forceinline__ uint32_t in_first_cta(const void *p) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_addr(p)));
+    return r;
 }
 
-template <int FMT>
-__device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
-                                        uint32_t accumulate) {
-    if constexpr (FMT == W4_FMT_MXFP4)
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
-            ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate) : "memory");
-    else
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
-            ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate) : "memory");
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-__device__ __forceinline__ void mma_commit(uint64_t *bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
-                 ::"r"(smem_addr(bar)) : "memory");
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
 }
 
-__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-                 ::"r"(smem_addr(dst)), "l"(src), "r"(bytes), "r"(smem_addr(bar)) : "memory");
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
 
-#define W4_FP4_TMEM_LD16(taddr, v)                                                                          \
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "                                                  \
-                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"                           \
-                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),       \
-                   "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),   \
-                   "=r"(v[14]), "=r"(v[15])                                                                  \
-                 : "r"(taddr))
-
-// gx * gw: one binary32 factor when it is a normal number or zero, else applied
-// in binary64 per value (the factor may leave binary32's range when the result
-// does not).
-struct Factor {
-    float f;
-    double d;
-    bool wide;
-    __device__ __forceinline__ Factor(const float *ga, const float *gb) {
-        d = (ga ? (double)__ldg(ga) : 1.0) * (gb ? (double)__ldg(gb) : 1.0);
-        f = (float)d;
-        const double m = fabs(d);
-        wide = !(d == 0.0 || (m >= 0x1p-126 && m < 0x1p128));
-    }
-    __device__ __forceinline__ float apply(float acc) const {
-        return wide ? (float)((double)acc * d) : acc * f;
-    }
-};
-
-__device__ __forceinline__ void store_one(void *y, size_t i, float v, int type) {
-    if (type == OUT_BF16) reinterpret_cast<__nv_bfloat16 *>(y)[i] = __float2bfloat16_rn(v);
-    else if (type == OUT_F16) reinterpret_cast<__half *>(y)[i] = __float2half_rn(v);
-    else reinterpret_cast<float *>(y)[i] = v;
-}
-
-template <int FMT, int NT, bool SWAP>
-__global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant__ CUtensorMap amap,
-                                                            const __grid_constant__ CUtensorMap bmap, const Params p) {
+template <int FMT, int NT>
+__global__ void __launch_bounds__(kThreads, 1)
+    gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
+                const __grid_constant__ CUtensorMap sxmap, const __grid_constant__ CUtensorMap swmap, const Params p) {
     using S = Shared<FMT, NT>;
     using C = Config<FMT, NT>;
+    constexpr int STAGES = C::STAGES;
     extern __shared__ uint8_t smem_raw[];
     S &sh = *reinterpret_cast<S *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const int pair0 = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     const int KT = (p.K + BK - 1) / BK;
-    const int ntiles = p.tiles_a * p.tiles_b;
+    const int ntiles = p.tiles_m * p.tiles_n;
     volatile int *abort = &sh.abort;
+    const unsigned long long limit = g_wait_limit_ns;
 
     if (threadIdx.x == 0) {
         sh.abort = 0;
@@ -190,138 +143,157 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
         }
         for (int i = 0; i < 2; i++) {
             mbar_init(&sh.acc_full[i], 1);
-            mbar_init(&sh.acc_empty[i], kEpiWarps);
+            mbar_init(&sh.acc_empty[i], 2 * kEpiWarps);
         }
         mbar_init(&sh.mma_done, 1);
         fence_mbar_init();
     }
     if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
-                     ::"r"(smem_addr(&sh.tmem_base)), "r"(C::TMEM_COLS));
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
+                     ::"r"(smem_addr(&sh.tmem_base)), "r"(512u));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
     }
     tc_fence_before();
     __syncthreads();
+    cluster_sync();
     tc_fence_after();
-    const uint32_t tmem = sh.tmem_base;
+    const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, sh.tmem_base, 0);
     // x may be the previous kernel's output (programmatic dependent launch)
     pdl_wait_prior_grid();
 
     if (warp == 0) {
         // ------------------------------ TMA producer ------------------------------
-        if (lane == 0) {
-            int it = 0;
-            for (int t = blockIdx.x; t < ntiles && !*abort; t += gridDim.x) {
-                const int ta = t % p.tiles_a, tb = t / p.tiles_a;
-                const int groups_b = min(C::GB, (p.rows_b + 127) / 128 - tb * NT / 128);
-                for (int kt = 0; kt < KT; kt++, it++) {
-                    const int s = it % STAGES;
-                    if (it >= STAGES) mbar_wait(&sh.empty[s], ((it / STAGES) - 1) & 1, abort);
-                    if (*abort) break;
-                    // scale tiles that exist in this stage (the last one of a row may be cut)
-                    const int nt = min(C::ST, p.tiles_k - kt * C::ST);
-                    mbar_arrive_expect_tx(&sh.full[s],
-                                          A_BYTES + C::B_BYTES + (uint32_t)(nt * (1 + groups_b)) * C::SF_TILE);
-                    tma_load_2d(sh.a[s], &amap, kt * (BK / 2), ta * BM, &sh.full[s]);
-                    tma_load_2d(sh.b[s], &bmap, kt * (BK / 2), tb * NT, &sh.full[s]);
-                    bulk_load(sh.sfa[s], p.sfa + ((size_t)ta * p.tiles_k + kt * C::ST) * C::SF_TILE,
-                              (uint32_t)nt * C::SF_TILE, &sh.full[s]);
-                    for (int g = 0; g < groups_b; g++)
-                        for (int c = 0; c < nt; c++)
-                            bulk_load(sh.sfb[s][c][g],
-                                      p.sfb + ((size_t)(tb * NT / 128 + g) * p.tiles_k + kt * C::ST + c) * C::SF_TILE,
-                                      C::SF_TILE, &sh.full[s]);
+        int it = 0;
+        bool stop = false;
+        for (int t = pair0; t < ntiles && !stop; t += pairs) {
+            const int tm = t % p.tiles_m, tn = t / p.tiles_m;
+            const int m0 = tm * 2 * BM + (int)rank * BM, n0 = tn * NT + (int)rank * (NT / 2);
+            for (int kt = 0; kt < KT; kt++, it++) {
+                const int s = it % STAGES;
+                if (it >= STAGES) pipe_wait(&sh.empty[s], ((it / STAGES) - 1) & 1, abort, limit);
+                // after an abort nothing more is loaded: the stage may not be free
+                stop = __any_sync(0xFFFFFFFFu, *abort != 0);
+                if (stop) break;
+                if (elect_one()) {
+                    if (rank == 0) mbar_arrive_expect_tx(&sh.full[s], 2 * C::STAGE_BYTES);
+                    const uint32_t full = in_first_cta(&sh.full[s]);
+                    tma_load_pair(sh.a[s], &xmap, kt * (BK / 2), m0, full);
+                    tma_load_pair(sh.b[s], &wmap, kt * (BK / 2), n0, full);
+                    // scale tiles as rows of 128 words; those past a row's last (read from
+                    // the next group, or zeros past the end) are not used
+                    tma_load_pair(sh.sfa[s], &sxmap, 0, (m0 / 128) * p.tiles_k + kt * C::ST, full);
+#pragma unroll
+                    for (int g = 0; g < C::GB; g++)
+                        tma_load_pair(sh.sfb[s][g], &swmap, 0, (tn * NT / 128 + g) * p.tiles_k + kt * C::ST, full);
                 }
             }
-            drain_ring(sh.full, STAGES, it);
         }
+        // no load may land and no commit arrive after this CTA has left: the first CTA
+        // waits for both CTAs' loads, each for the MMAs' arrivals on its own barriers,
+        // and both meet in the cluster barrier at the end
+        if (rank == 0) drain_ring(sh.full, STAGES, it);
+        for (int i = max(0, it - STAGES); i < it; i++)
+            pipe_wait(&sh.empty[i % STAGES], (i / STAGES) & 1, abort, limit);
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------- MMA issuer -------------------------------
-        if (lane == 0) {
+        if (rank == 0) {
             int it = 0, lt = 0;
+            bool stop = false;
             const int steps = (p.K + 63) / 64;
-            for (int t = blockIdx.x; t < ntiles; t += gridDim.x, lt++) {
-                const int b = lt & 1;
-                const uint32_t acc = tmem + (uint32_t)b * C::ACC_COLS;
-                // a B tile narrower than 128 rows starts inside its scale tile
-                const uint32_t sfb_shift = (uint32_t)(((t / p.tiles_a) * NT % 128) / 32);
-                if (lt >= 2) mbar_wait(&sh.acc_empty[b], ((lt >> 1) - 1) & 1, abort);
-                tc_fence_after();
+            const uint32_t sfa = tmem + C::SF_COL0, sfb = sfa + 4 * C::ST;
+            for (int t = pair0; t < ntiles && !stop; t += pairs, lt++) {
+                const uint32_t acc = tmem + (lt & 1 ? C::ACC1 : 0u);
+                const uint32_t shift = (uint32_t)(((t / p.tiles_m) * NT % 128) / 32);
+                if (C::OVERLAP > 0) {   // the columns shared with the previous tile's accumulator are drained
+                    if (lt >= 1) pipe_wait(&sh.acc_empty[(lt - 1) & 1], ((lt - 1) >> 1) & 1, abort, limit);
+                } else {                // this accumulator is
+                    if (lt >= 2) pipe_wait(&sh.acc_empty[lt & 1], ((lt >> 1) - 1) & 1, abort, limit);
+                }
                 for (int kt = 0; kt < KT; kt++, it++) {
                     const int s = it % STAGES;
-                    mbar_wait(&sh.full[s], (it / STAGES) & 1, abort);
-                    if (*abort) break;
+                    pipe_wait(&sh.full[s], (it / STAGES) & 1, abort, limit);
+                    stop = __any_sync(0xFFFFFFFFu, *abort != 0);
+                    if (stop) break;
                     tc_fence_after();
-                    // the stage's own scale columns: free once the stage is (its MMAs have completed)
-                    const uint32_t sfa = tmem + C::SF_COL0 + (uint32_t)s * C::SF_COLS, sfb = sfa + 4 * C::ST;
-                    const uint32_t a0 = smem_addr(sh.a[s]), b0 = smem_addr(sh.b[s]);
-                    for (int c = 0; c < C::ST; c++) {
-                        if (kt * C::ST + c >= p.tiles_k) break;
-                        copy_scales(sfa + 4 * c, scale_desc(smem_addr(sh.sfa[s][c])));
-                        for (int g = 0; g < C::GB; g++)
-                            copy_scales(sfb + 4 * (c * C::GB + g), scale_desc(smem_addr(sh.sfb[s][c][g])));
-                    }
+                    if (elect_one()) {
+                        const uint32_t a = codes_desc(smem_addr(sh.a[s])), b = codes_desc(smem_addr(sh.b[s]));
+                        const uint32_t fa = scale_desc(smem_addr(sh.sfa[s])), fb = scale_desc(smem_addr(sh.sfb[s]));
 #pragma unroll
-                    for (int j = 0; j < BK / 64; j++) {
-                        if (kt * (BK / 64) + j >= steps) break;
-                        const int c = j / Scales<FMT>::STEPS_PER_TILE;
-                        const uint32_t id = Scales<FMT>::STEPS_PER_TILE == 2 ? (uint32_t)(j & 1) * 2u : 0u;
-                        mma_fp4<FMT>(acc, sw128_desc(a0 + 32 * j), sw128_desc(b0 + 32 * j),
-                                     C::IDESC | (id << 4) | (id << 29), sfa + 4 * c, sfb + 4 * c * C::GB + sfb_shift,
-                                     (kt | j) ? 1u : 0u);
+                        for (int c = 0; c < C::ST; c++) {
+                            copy_scales<2>(sfa + 4 * c, fa + c * (SF_TILE / 16));
+#pragma unroll
+                            for (int g = 0; g < C::GB; g++)
+                                copy_scales<2>(sfb + 4 * (c * C::GB + g), fb + (g * C::ST + c) * (SF_TILE / 16));
+                        }
+#pragma unroll
+                        for (int j = 0; j < BK / 64; j++) {
+                            const int c = j / Scales<FMT>::STEPS_PER_TILE;
+                            if (kt * (BK / 64) + j < steps)
+                                mma_fp4<FMT, 2>(acc, a + 2 * j, b + 2 * j, idesc<FMT>(2 * BM, NT) | scale_ids<FMT>(j),
+                                                sfa + 4 * c, sfb + 4 * c * C::GB + shift, (kt | j) ? 1u : 0u);
+                        }
+                        commit_pair(&sh.empty[s]);
+                        if (kt == KT - 1) commit_pair(&sh.acc_full[lt & 1]);
                     }
-                    mma_commit(&sh.empty[s]);
+                    __syncwarp();
                 }
-                if (*abort) break;
-                mma_commit(&sh.acc_full[b]);
             }
-            // tensor memory is released after the final barrier: every MMA and copy
-            // this thread issued must have completed by then (also after an abort)
-            mma_commit(&sh.mma_done);
+            // tensor memory is released after the cluster barrier: every MMA and copy
+            // issued must have completed by then (also after an abort)
+            if (elect_one())
+                asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];"
+                             ::"r"(smem_addr(&sh.mma_done)) : "memory");
+            __syncwarp();
             mbar_wait_bounded(&sh.mma_done, 0);
         }
         __syncwarp();
     } else {
         // -------------------------------- epilogue --------------------------------
-        const int q = warp & 3;
-        const Factor fac(p.ga, p.gb);
+        const int q = warp & 3, half = (warp - kEpiWarp0) >> 2;
+        const Factor fac(p.gx, p.gw);
         int lt = 0;
-        for (int t = blockIdx.x; t < ntiles; t += gridDim.x, lt++) {
+        for (int t = pair0; t < ntiles; t += pairs, lt++) {
             const int b = lt & 1;
-            const int ra = (t % p.tiles_a) * BM + q * 32 + lane;   // this lane's row of A
-            const int rb0 = (t / p.tiles_a) * NT;
+            const int m = (t % p.tiles_m) * 2 * BM + (int)rank * BM + q * 32 + lane;
+            const int n0 = (t / p.tiles_m) * NT;
             // on expiry (abort) the accumulator is garbage, but the warp stays together
-            mbar_wait(&sh.acc_full[b], (lt >> 1) & 1, abort);
+            pipe_wait(&sh.acc_full[b], (lt >> 1) & 1, abort, limit);
             __syncwarp();
             tc_fence_after();
-            for (int c = 0; c < NT / 16; c++) {
-                uint32_t v[16];
-                W4_FP4_TMEM_LD16(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * C::ACC_COLS + c * 16), v);
+            const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + (b ? C::ACC1 : 0u);
+            const uint32_t empty = in_first_cta(&sh.acc_empty[b]);
+            // shared columns first: the last of accumulator 0, the first of accumulator 1
+#pragma unroll 1
+            for (int i = half; i < NT / CHUNK; i += 2) {
+                const int c = b ? i : NT / CHUNK - 1 - i;
+                uint32_t v[CHUNK];
+                tmem_ld32(acc + (uint32_t)(c * CHUNK), v);
                 asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-                for (int j = 0; j < 16; j++) {
-                    const int rb = rb0 + c * 16 + j;
-                    if (ra < p.rows_a && rb < p.rows_b) {
-                        const size_t i = SWAP ? (size_t)rb * p.ldy + ra : (size_t)ra * p.ldy + rb;
-                        store_one(p.y, i, fac.apply(__uint_as_float(v[j])), p.out_type);
-                    }
+                const bool last = i + 2 >= NT / CHUNK;
+                const bool release = C::OVERLAP > 0 ? i == half : last;
+                if (release) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) arrive_cluster(empty);
                 }
+                if (m < p.M)
+                    store_values(p.y, (size_t)m * p.ldy + n0 + c * CHUNK, n0 + c * CHUNK, p.N, p.out_type, p.vec, fac, v);
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.acc_empty[b]);
         }
         __syncwarp();
     }
 
     tc_fence_before();
     __syncthreads();
+    cluster_sync();
     if (warp == 1) {
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::TMEM_COLS));
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
     }
 }
+
+}  // namespace pair
 
 }  // namespace fgemm
 
