@@ -142,7 +142,7 @@ bool codes_map(CUtensorMap &map, const uint8_t *codes, int rows, int K, int box_
                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int FMT, int NT, bool SWAP>
+template <int FMT, int NT>
 w4_status launch_skinny(const w4_fp4 *a, const w4_fp4 *b, void *y, long long ldy, int out_type, bool early_w,
                       cudaStream_t st) {
     using namespace fgemm;
@@ -154,7 +154,7 @@ w4_status launch_skinny(const w4_fp4 *a, const w4_fp4 *b, void *y, long long ldy
     if (device_sms(sms) != W4_OK) return W4_ERR_CUDA;
     constexpr size_t smem = sizeof(Shared<FMT, NT>) + 1024;
     static_assert(smem <= 227 * 1024, "shared memory of the product");
-    auto kernel = gemm_kernel<FMT, NT, SWAP>;
+    auto kernel = skinny::gemm_kernel<FMT, NT>;
     if (!set_smem_limit(reinterpret_cast<const void *>(kernel), smem)) return W4_ERR_CUDA;
     Params p;
     p.sfa = a->scales;
@@ -201,10 +201,20 @@ bool scales_map(CUtensorMap &map, const uint8_t *scales, size_t bytes, int tiles
                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Bytes of the widest store that every output row is aligned for.
-int store_bytes(const void *y, long long ldy, int type) {
-    const uintptr_t a = reinterpret_cast<uintptr_t>(y) | (uintptr_t)(ldy * type_size(type));
-    return a % 32 == 0 ? 32 : a % 16 == 0 ? 16 : 0;
+// y as boxes of 32 rows x 128 bytes, 128-byte swizzle (rows on 16 bytes).
+bool output_map(CUtensorMap &map, void *y, int rows, int cols, long long ldy, int type) {
+    PFN_encodeTiled enc = get_encode_tiled();
+    const int size = type_size(type);
+    const CUtensorMapDataType t = type == W4_TYPE_BF16  ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                  : type == W4_TYPE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                        : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)ldy * size};
+    const cuuint32_t box[2] = {(cuuint32_t)(128 / size), 32};
+    const cuuint32_t estr[2] = {1, 1};
+    return enc && enc(&map, t, 2, y, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int FMT, int NT>
@@ -226,16 +236,19 @@ w4_status launch_pair(const w4_fp4 *w, const w4_fp4 *x, void *y, long long ldy, 
     pair::Params p;
     p.gx = FMT == W4_FMT_NVFP4 ? x->global_scale : nullptr;
     p.gw = FMT == W4_FMT_NVFP4 ? w->global_scale : nullptr;
-    p.y = y;
-    p.ldy = ldy;
-    p.M = x->rows;
-    p.N = w->rows;
+    p.out.y = y;
+    p.out.ldy = ldy;
+    p.out.rows = x->rows;
+    p.out.cols = w->rows;
+    p.out.type = out_type;
+    // a box is clipped to the tensor in units of 16 bytes, so a row must end on one
+    p.out.tma = rows16(ldy, out_type) && rows16(w->rows, out_type);
+    CUtensorMap ymap = xmap;   // not read without p.out.tma
+    if (p.out.tma && !output_map(ymap, y, x->rows, w->rows, ldy, out_type)) return W4_ERR_CUDA;
     p.K = x->K;
     p.tiles_m = (x->rows + 2 * BM - 1) / (2 * BM);
     p.tiles_n = (w->rows + NT - 1) / NT;
     p.tiles_k = fp4::scale_tiles_k(FMT, x->K);
-    p.out_type = out_type;
-    p.vec = store_bytes(y, ldy, out_type);
     const long long ntiles = (long long)p.tiles_m * p.tiles_n;
     if (ntiles > kMaxBlocks) return W4_ERR_UNSUPPORTED;
     cudaLaunchConfig_t cfg = {};
@@ -252,7 +265,7 @@ w4_status launch_pair(const w4_fp4 *w, const w4_fp4 *x, void *y, long long ldy, 
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    if (cudaLaunchKernelEx(&cfg, kernel, xmap, wmap, sxmap, swmap, p) != cudaSuccess) return W4_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, kernel, xmap, wmap, sxmap, swmap, ymap, p) != cudaSuccess) return W4_ERR_CUDA;
     return launch_status();
 }
 
@@ -260,9 +273,9 @@ template <int FMT>
 w4_status gemm_fmt(const w4_fp4 *w, const w4_fp4 *x, void *y, long long ldy, int out_type, bool early_w,
                    cudaStream_t st) {
     const int M = x->rows;
-    if (M <= 16) return launch_skinny<FMT, 16, true>(w, x, y, ldy, out_type, early_w, st);
-    if (M <= 64) return launch_skinny<FMT, 64, true>(w, x, y, ldy, out_type, early_w, st);
-    if (M <= 128) return launch_skinny<FMT, 128, true>(w, x, y, ldy, out_type, early_w, st);
+    if (M <= 16) return launch_skinny<FMT, 16>(w, x, y, ldy, out_type, early_w, st);
+    if (M <= 64) return launch_skinny<FMT, 64>(w, x, y, ldy, out_type, early_w, st);
+    if (M <= 128) return launch_skinny<FMT, 128>(w, x, y, ldy, out_type, early_w, st);
     const char *e = getenv("W4_NT");
     const int nt = e ? atoi(e) : 256;
     if (nt == 192) return launch_pair<FMT, 192>(w, x, y, ldy, out_type, st);

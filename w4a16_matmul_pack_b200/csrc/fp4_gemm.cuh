@@ -36,8 +36,8 @@ constexpr int kEpiWarps = 8;
 constexpr int kEpiWarp0 = 2;
 constexpr int kWarps = kEpiWarp0 + kEpiWarps;
 constexpr int kThreads = kWarps * 32;
-constexpr int CHUNK = 32;                // accumulator columns per epilogue step
-constexpr uint32_t kSmemBudget = 224 * 1024;
+constexpr int CHUNK = 64;                // accumulator columns per epilogue step
+constexpr uint32_t kSmemBudget = 225 * 1024 - kEpiWarps * OUT_BYTES;
 
 template <int FMT, int NT>
 struct Config {
@@ -54,8 +54,7 @@ struct Config {
     static constexpr uint32_t SF_COL0 = 512 - SF_COLS;
     static constexpr uint32_t ACC1 = NT < SF_COL0 - NT ? NT : SF_COL0 - NT;  // first column of accumulator 1
     static constexpr int OVERLAP = NT - (int)ACC1;                           // columns the accumulators share
-    static constexpr int OVERLAP_CHUNKS = (OVERLAP + CHUNK - 1) / CHUNK;
-    static_assert(NT % 64 == 0 && NT <= 256 && STAGES >= 3 && OVERLAP <= 2 * CHUNK, "tile");
+    static_assert(NT % 64 == 0 && NT >= 2 * CHUNK && NT <= 256 && STAGES >= 3 && OVERLAP <= CHUNK, "tile");
 };
 
 template <int FMT, int NT>
@@ -63,6 +62,7 @@ struct Shared {
     using C = Config<FMT, NT>;
     uint8_t a[C::STAGES][A_BYTES];                 // 1024-byte aligned (swizzle atoms)
     uint8_t b[C::STAGES][C::B_BYTES];
+    uint8_t out[kEpiWarps][OUT_BYTES];             // 1024-byte aligned
     uint8_t sfa[C::STAGES][C::ST][SF_TILE];
     uint8_t sfb[C::STAGES][C::GB][C::ST][SF_TILE];
     uint64_t full[C::STAGES], empty[C::STAGES];    // full: the first CTA's, for both CTAs' loads
@@ -74,12 +74,9 @@ struct Shared {
 
 struct Params {
     const float *gx, *gw;          // global scales (NVFP4) or null
-    void *y;
-    long long ldy;
-    int M, N, K;
+    Output out;
+    int K;
     int tiles_m, tiles_n, tiles_k; // tiles_k: scale tiles along K
-    int out_type;
-    int vec;                       // bytes of the widest aligned store: 32, 16 or 0 (single values)
 };
 
 // Arrives on the barrier at this offset in both CTAs once the MMAs and copies
@@ -121,7 +118,8 @@ __device__ __forceinline__ void cluster_sync() {
 template <int FMT, int NT>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
-                const __grid_constant__ CUtensorMap sxmap, const __grid_constant__ CUtensorMap swmap, const Params p) {
+                const __grid_constant__ CUtensorMap sxmap, const __grid_constant__ CUtensorMap swmap,
+                const __grid_constant__ CUtensorMap ymap, const __grid_constant__ Params p) {
     using S = Shared<FMT, NT>;
     using C = Config<FMT, NT>;
     constexpr int STAGES = C::STAGES;
@@ -255,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int lt = 0;
         for (int t = pair0; t < ntiles; t += pairs, lt++) {
             const int b = lt & 1;
-            const int m = (t % p.tiles_m) * 2 * BM + (int)rank * BM + q * 32 + lane;
+            const int m0 = (t % p.tiles_m) * 2 * BM + (int)rank * BM + q * 32;
             const int n0 = (t / p.tiles_m) * NT;
             // on expiry (abort) the accumulator is garbage, but the warp stays together
             pipe_wait(&sh.acc_full[b], (lt >> 1) & 1, abort, limit);
@@ -267,20 +265,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int i = half; i < NT / CHUNK; i += 2) {
                 const int c = b ? i : NT / CHUNK - 1 - i;
-                uint32_t v[CHUNK];
-                tmem_ld32(acc + (uint32_t)(c * CHUNK), v);
-                asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-                const bool last = i + 2 >= NT / CHUNK;
-                const bool release = C::OVERLAP > 0 ? i == half : last;
-                if (release) {
+                float v[CHUNK];
+                tmem_ld64(acc + (uint32_t)(c * CHUNK), v);
+                if (C::OVERLAP > 0 ? i == half : i + 2 >= NT / CHUNK) {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) arrive_cluster(empty);
                 }
-                if (m < p.M)
-                    store_values(p.y, (size_t)m * p.ldy + n0 + c * CHUNK, n0 + c * CHUNK, p.N, p.out_type, p.vec, fac, v);
+                apply_factor(fac, v);
+                store_rows(p.out, &ymap, sh.out[warp - kEpiWarp0], m0, n0 + c * CHUNK, v);
             }
         }
+        store_rows_done();
         __syncwarp();
     }
 

@@ -143,16 +143,7 @@ struct Factor {
         const double m = fabs(d);
         wide = !(d == 0.0 || (m >= 0x1p-126 && m < 0x1p128));
     }
-    __device__ __forceinline__ float apply(float acc) const {
-        return wide ? (float)((double)acc * d) : acc * f;
-    }
 };
-
-__device__ __forceinline__ void store_one(void *y, size_t i, float v, int type) {
-    if (type == OUT_BF16) reinterpret_cast<__nv_bfloat16 *>(y)[i] = __float2bfloat16_rn(v);
-    else if (type == OUT_F16) reinterpret_cast<__half *>(y)[i] = __float2half_rn(v);
-    else reinterpret_cast<float *>(y)[i] = v;
-}
 
 // 32 consecutive columns of this warp's 32 lanes.
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
@@ -166,64 +157,109 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
         : "r"(taddr));
 }
 
-// One 32-byte store: a whole sector per lane.
-__device__ __forceinline__ void store32(void *p, const uint32_t *w) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
-                 ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                 : "memory");
+// 64 columns of this warp's 32 lanes (one row of the output each, or one column of
+// it transposed), times the factor.
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, float (&v)[64]) {
+    uint32_t a[32], b[32];
+    tmem_ld32(taddr, a);
+    tmem_ld32(taddr + 32, b);
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 32; i++) v[i] = __uint_as_float(a[i]), v[32 + i] = __uint_as_float(b[i]);
 }
 
-// 32 consecutive values of one output row, from column n.  vec: bytes of the
-// widest store the rows are aligned for (32, 16, or 0 for single values); the
-// lanes of a warp hold different rows, so a 32-byte store writes whole sectors.
-__device__ __forceinline__ void store_values(void *y, size_t at, int n, int N, int type, int vec, const Factor &fac,
-                                             const uint32_t (&v)[32]) {
-    if (n >= N) return;
-    if (vec && n + 32 <= N) {
-        if (type == OUT_F32) {
-            float *o = reinterpret_cast<float *>(y) + at;
+template <int n>
+__device__ __forceinline__ void apply_factor(const Factor &f, float (&v)[n]) {
+    if (f.wide) {
+#pragma unroll 1
+        for (int i = 0; i < n; i += 8)
 #pragma unroll
-            for (int j = 0; j < 32; j += 8) {
-                uint32_t w[8];
+            for (int j = 0; j < n; j++)
+                if (j >= i && j < i + 8) v[j] = (float)((double)v[j] * f.d);
+    } else {
 #pragma unroll
-                for (int i = 0; i < 8; i++) w[i] = __float_as_uint(fac.apply(__uint_as_float(v[j + i])));
-                if (vec == 32) {
-                    store32(o + j, w);
-                } else {
-                    *reinterpret_cast<uint4 *>(o + j) = make_uint4(w[0], w[1], w[2], w[3]);
-                    *reinterpret_cast<uint4 *>(o + j + 4) = make_uint4(w[4], w[5], w[6], w[7]);
-                }
-            }
-        } else {
-            uint16_t *o = reinterpret_cast<uint16_t *>(y) + at;
-#pragma unroll
-            for (int j = 0; j < 32; j += 16) {
-                uint32_t w[8];
-#pragma unroll
-                for (int i = 0; i < 8; i++) {
-                    const float a = fac.apply(__uint_as_float(v[j + 2 * i]));
-                    const float b = fac.apply(__uint_as_float(v[j + 2 * i + 1]));
-                    if (type == OUT_BF16) {
-                        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-                        w[i] = *reinterpret_cast<const uint32_t *>(&h);
-                    } else {
-                        const __half2 h = __floats2half2_rn(a, b);
-                        w[i] = *reinterpret_cast<const uint32_t *>(&h);
-                    }
-                }
-                if (vec == 32) {
-                    store32(o + j, w);
-                } else {
-                    *reinterpret_cast<uint4 *>(o + j) = make_uint4(w[0], w[1], w[2], w[3]);
-                    *reinterpret_cast<uint4 *>(o + j + 8) = make_uint4(w[4], w[5], w[6], w[7]);
-                }
-            }
-        }
-        return;
+        for (int i = 0; i < n; i++) v[i] *= f.f;
     }
+}
+
+// Two values as 16-bit words of `type` (OUT_BF16 or OUT_F16).
+__device__ __forceinline__ uint32_t pack16(float a, float b, int type) {
+    if (type == OUT_BF16) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// Where an epilogue writes y [rows][cols].
+struct Output {
+    void *y;
+    long long ldy;
+    int rows, cols, type;
+    int tma;             // the rows start and end on 16 bytes: boxes by TMA
+};
+
+constexpr uint32_t OUT_BYTES = 32 * 128;   // staging of one epilogue warp: 32 rows x 128 bytes
+
+// 32 rows x 64 columns of y at (row0, col0) from the lanes of a warp (lane = row).
+// A lane's values are consecutive in a row of y, and the rows of a warp far apart:
+// written straight from registers every store touches 32 rows (3.4 us for a 128 x 256
+// tile); so the rows are gathered in shared memory (128 bytes each, 128-byte
+// swizzle, no bank conflicts) and leave as one TMA box, or row by row where y's rows
+// do not start and end on 16 bytes.
+__device__ __forceinline__ void store_rows(const Output &o, const CUtensorMap *map, uint8_t *buf, int row0, int col0,
+                                           const float (&v)[64]) {
+    const int lane = threadIdx.x & 31;
+    const bool f32 = o.type == OUT_F32;
+    const uint32_t row = smem_addr(buf) + (uint32_t)lane * 128;
 #pragma unroll
-    for (int j = 0; j < 32; j++)
-        if (n + j < N) store_one(y, at + j, fac.apply(__uint_as_float(v[j])), type);
+    for (int half = 0; half < 2; half++) {
+        if (half == 1 && !f32) break;
+        const int col = col0 + half * 32, ncols = f32 ? 32 : 64;
+        if (row0 >= o.rows || col >= o.cols) break;
+        // the previous box has been read
+        if (elect_one()) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                w[i] = f32 ? __float_as_uint(v[half * 32 + 4 * j + i])
+                           : pack16(v[8 * j + 2 * i], v[8 * j + 2 * i + 1], o.type);
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};"
+                         ::"r"(row + (uint32_t)((j ^ (lane & 7)) * 16)), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                         : "memory");
+        }
+        if (o.tma) {
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (elect_one())
+                asm volatile(
+                    "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];\n\t"
+                    "cp.async.bulk.commit_group;"
+                    ::"l"(reinterpret_cast<uint64_t>(map)), "r"(col), "r"(row0), "r"(smem_addr(buf)) : "memory");
+        } else {
+            __syncwarp();
+            const int size = f32 ? 4 : 2;
+            for (int r = 0; r < 32 && row0 + r < o.rows; r++) {
+                for (int c = lane; c < ncols && col + c < o.cols; c += 32) {
+                    const uint8_t *src = buf + r * 128 + (((c * size) >> 4) ^ (r & 7)) * 16 + ((c * size) & 15);
+                    const size_t at = (size_t)(row0 + r) * o.ldy + col + c;
+                    if (f32) reinterpret_cast<uint32_t *>(o.y)[at] = *reinterpret_cast<const uint32_t *>(src);
+                    else reinterpret_cast<uint16_t *>(o.y)[at] = *reinterpret_cast<const uint16_t *>(src);
+                }
+            }
+            __syncwarp();
+        }
+    }
+}
+
+// Before the warp's staging buffer goes out of use: its boxes have been written.
+__device__ __forceinline__ void store_rows_done() {
+    if (elect_one()) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    __syncwarp();
 }
 
 }  // namespace fgemm

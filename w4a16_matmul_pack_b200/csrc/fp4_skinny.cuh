@@ -1,9 +1,9 @@
 // fp4_skinny.cuh -- W4A4 product with one CTA per tile (sm_100a): few tokens.
 // (see fp4_mma.cuh for the instructions both product kernels use)
 //
-// Tile: 128 rows of the operand A (tensor-memory lanes) x NT rows of B x 256 k
-// per stage.  SWAP = true (few tokens): A is w, so that 128 x NT wastes no work on
-// missing tokens, and lanes run along n.  SWAP = false: A is x.
+// Tile: 128 rows of w (the operand A, tensor-memory lanes) x NT tokens (B) x 256 k
+// per stage: no work is wasted on missing tokens, and the lanes of an epilogue
+// store run along a row of y.
 //
 // Warp roles (6 warps): 0 TMA producer; 1 tensor-memory allocation, scale copies
 // and MMAs (one lane); 2-5 epilogue (warp w reads lanes 32 (w % 4) .. + 31).
@@ -61,9 +61,10 @@ struct Params {
     int early_w;                   // the weights may be read before the previous kernel has completed
 };
 
-template <int FMT, int NT, bool SWAP>
+template <int FMT, int NT>
 __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant__ CUtensorMap amap,
-                                                            const __grid_constant__ CUtensorMap bmap, const Params p) {
+                                                            const __grid_constant__ CUtensorMap bmap,
+                                                            const __grid_constant__ Params p) {
     using S = Shared<FMT, NT>;
     using C = Config<FMT, NT>;
     extern __shared__ uint8_t smem_raw[];
@@ -183,23 +184,27 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
         int lt = 0;
         for (int t = blockIdx.x; t < ntiles; t += gridDim.x, lt++) {
             const int b = lt & 1;
-            const int ra = (t % p.tiles_a) * BM + q * 32 + lane;   // this lane's row of A
-            const int rb0 = (t / p.tiles_a) * NT;
+            const int n = (t % p.tiles_a) * BM + q * 32 + lane;    // this lane's row of w
             // on expiry (abort) the accumulator is garbage, but the warp stays together
             pipe_wait(&sh.acc_full[b], (lt >> 1) & 1, abort, limit);
             __syncwarp();
             tc_fence_after();
             for (int c = 0; c < NT / 16; c++) {
-                uint32_t v[16];
-                W4_FP4_TMEM_LD16(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * C::ACC_COLS + c * 16), v);
+                uint32_t r[16];
+                W4_FP4_TMEM_LD16(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * C::ACC_COLS + c * 16), r);
                 asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+                float v[16];
+#pragma unroll
+                for (int j = 0; j < 16; j++) v[j] = __uint_as_float(r[j]);
+                apply_factor(fac, v);
+                if (n >= p.rows_a) continue;
+                const int m0 = (t / p.tiles_a) * NT + c * 16, count = min(16, p.rows_b - m0);
 #pragma unroll
                 for (int j = 0; j < 16; j++) {
-                    const int rb = rb0 + c * 16 + j;
-                    if (ra < p.rows_a && rb < p.rows_b) {
-                        const size_t i = SWAP ? (size_t)rb * p.ldy + ra : (size_t)ra * p.ldy + rb;
-                        store_one(p.y, i, fac.apply(__uint_as_float(v[j])), p.out_type);
-                    }
+                    if (j >= count) break;
+                    const size_t i = (size_t)(m0 + j) * p.ldy + n;
+                    if (p.out_type == OUT_F32) reinterpret_cast<float *>(p.y)[i] = v[j];
+                    else reinterpret_cast<uint16_t *>(p.y)[i] = (uint16_t)pack16(v[j], v[j], p.out_type);
                 }
             }
             tc_fence_before();
