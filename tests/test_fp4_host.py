@@ -10,7 +10,21 @@ import w4a16_matmul_pack_b200 as W4
 from w4a16_matmul_pack_b200 import build as B
 
 ARG, ALIGN, UNSUPPORTED, WORKSPACE = 1, 2, 3, 7
-P = ctypes.c_void_p
+P, I, LL, F = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_float
+
+
+class Fp4(ctypes.Structure):
+    """w4_fp4 of include/w4a16.h."""
+    _fields_ = [("fmt", I), ("rows", I), ("K", I), ("codes", P), ("scales", P), ("global_scale", P)]
+
+
+class Norm(ctypes.Structure):
+    """w4_norm of include/w4a16.h."""
+    _fields_ = ([(n, I) for n in ("type", "M", "D")] + [(n, P) for n in ("y", "h", "w_post", "w_pre", "gate")]
+                + [(n, LL) for n in ("ldy", "ldh", "ldgate")] + [(n, I) for n in ("gate_rows", "gate_act")]
+                + [(n, F) for n in ("residual_scale", "block_scale", "eps", "weight_offset")]
+                + [("h_out", P), ("ldh_out", LL), ("z", P), ("ldz", LL), ("quant_fmt", I), ("scale_rule", I)]
+                + [(n, P) for n in ("global_scale", "codes", "scales", "d_status")])
 
 
 @pytest.fixture(scope="module")
@@ -24,6 +38,15 @@ def lib():
 def test_scale_bytes(lib, rows, K, mx, nv):
     assert lib.fp4_scale_bytes(W4.FMT_MXFP4, rows, K) == mx
     assert lib.fp4_scale_bytes(W4.FMT_NVFP4, rows, K) == nv
+    assert W4.fp4_scale_bytes(W4.FMT_MXFP4, rows, K) == mx and W4.fp4_scale_bytes(W4.FMT_NVFP4, rows, K) == nv
+
+
+def test_packed_structs_are_the_headers():
+    """The binding packs its structs as bytes: the same layout as the C structs."""
+    v = (5, 7, 64, 1 << 40, 2 << 40, 3 << 40)
+    assert W4._pack_fp4(*v) == bytes(Fp4(*v))
+    v = (1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 11, 12, 1, 1.5, 2.5, 3.5, 4.5, 13, 14, 15, 16, 5, 1, 17, 18, 19, 20)
+    assert W4._pack_norm(*v) == bytes(Norm(*v))
 
 
 def test_scale_bytes_of_bad_shapes(lib):
@@ -46,7 +69,7 @@ def test_quantize_refusals(lib):
 
 
 def operand(fmt=5, rows=8, K=64, codes=16, scales=16, g=None):
-    return W4._Fp4(fmt, rows, K, codes, scales, g)
+    return Fp4(fmt, rows, K, codes, scales, g)
 
 
 def test_product_refusals(lib):
@@ -70,6 +93,10 @@ def test_linear_refusals(lib):
     need = lib.w4a4_workspace_bytes(ctypes.byref(w), 3)
     assert need >= 3 * 32 + 512
     assert lib.w4a4_workspace_bytes(ctypes.byref(w), 0) == 0
+    for M in (1, 3, 77, 129, 1000):       # the binding's own arithmetic
+        for fmt, K in ((5, 64), (5, 2592), (1, 96)):
+            c = operand(fmt, 8, K, g=16 if fmt == 1 else None)
+            assert W4.w4a4_workspace_bytes(c, M) == lib.w4a4_workspace_bytes(ctypes.byref(c), M) > 0
 
     def call(w=w, x=P(16), type=0, ldx=64, M=3, rule=0, g=None, y=P(16), out=0, ldy=8, ws=P(256), n=need):
         return lib.w4a4_linear(ctypes.byref(w), x, type, ldx, M, rule, g, y, out, ldy, ws, n, None, None)
@@ -84,7 +111,7 @@ def test_norm_refusals(lib):
     def call(**kw):
         d = dict(type=0, M=2, D=64, y=16, ldy=64, residual_scale=1.0, block_scale=1.0, eps=1e-6, z=16, ldz=64)
         d.update(kw)
-        return lib.w4_block_norm(ctypes.byref(W4._Norm(**d)), None)
+        return lib.w4_block_norm(ctypes.byref(Norm(**d)), None)
     assert lib.w4_block_norm(None, None) == ARG
     assert call(y=None) == ARG and call(z=None) == ARG and call(M=0) == ARG and call(D=0) == ARG
     assert call(type=4) == ARG and call(ldy=63) == ARG and call(ldz=10) == ARG

@@ -62,23 +62,6 @@ class W4Error(RuntimeError):
         super().__init__(f"{what}: {lib().w4_status_string(status).decode()}")
 
 
-class _Fp4(ctypes.Structure):
-    _fields_ = [("fmt", ctypes.c_int), ("rows", ctypes.c_int), ("K", ctypes.c_int),
-                ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("global_scale", ctypes.c_void_p)]
-
-
-class _Norm(ctypes.Structure):
-    _fields_ = ([(n, ctypes.c_int) for n in ("type", "M", "D")]
-                + [(n, ctypes.c_void_p) for n in ("y", "h", "w_post", "w_pre", "gate")]
-                + [(n, ctypes.c_longlong) for n in ("ldy", "ldh", "ldgate")]
-                + [(n, ctypes.c_int) for n in ("gate_rows", "gate_act")]
-                + [(n, ctypes.c_float) for n in ("residual_scale", "block_scale", "eps", "weight_offset")]
-                + [("h_out", ctypes.c_void_p), ("ldh_out", ctypes.c_longlong),
-                   ("z", ctypes.c_void_p), ("ldz", ctypes.c_longlong),
-                   ("quant_fmt", ctypes.c_int), ("scale_rule", ctypes.c_int)]
-                + [(n, ctypes.c_void_p) for n in ("global_scale", "codes", "scales", "d_status")])
-
-
 class _Weights(ctypes.Structure):
     _fields_ = [("fmt", ctypes.c_int), ("K", ctypes.c_int), ("N", ctypes.c_int),
                 ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
@@ -97,7 +80,7 @@ def lib():
                                "`python -m w4a16_matmul_pack_b200.build` (nvcc, sm_100a)")
         L = ctypes.CDLL(_LIB_PATH)
         P, I, U, S = ctypes.c_void_p, ctypes.c_int, ctypes.c_uint, ctypes.c_size_t
-        WP, FP, LL = ctypes.POINTER(_Weights), ctypes.POINTER(_Fp4), ctypes.c_longlong
+        WP, LL = ctypes.POINTER(_Weights), ctypes.c_longlong
         sig = {
             "pack_nvfp4": ([P, I, I, I, I, P, P, P, P, S, P, P], I),
             "pack_nvfp4_ex": ([P, I, I, I, I, P, P, P, P, P, S, P, P], I),
@@ -117,12 +100,12 @@ def lib():
             "w4_set_wait_limit": ([ctypes.c_ulonglong], I),
             "fp4_scale_bytes": ([I, I, I], S),
             "fp4_quantize": ([P, I, LL, I, I, I, I, P, P, P, P, P], I),
-            "fp4_dequantize": ([FP, P, I, LL, P], I),
+            "fp4_dequantize": ([P, P, I, LL, P], I),
             "fp4_tile_scales": ([I, I, I, P, P, P], I),
-            "w4a4_gemm": ([FP, FP, P, I, LL, U, P], I),
-            "w4a4_workspace_bytes": ([FP, I], S),
-            "w4a4_linear": ([FP, P, I, LL, I, I, P, P, I, LL, P, S, P, P], I),
-            "w4_block_norm": ([ctypes.POINTER(_Norm), P], I),
+            "w4a4_gemm": ([P, P, P, I, LL, U, P], I),
+            "w4a4_workspace_bytes": ([P, I], S),
+            "w4a4_linear": ([P, P, I, LL, I, I, P, P, I, LL, P, S, P, P], I),
+            "w4_block_norm": ([P, P], I),
             "w4_status_string": ([I], ctypes.c_char_p),
             "w4_version": ([], ctypes.c_char_p),
         }
@@ -380,115 +363,164 @@ def w4a16_gemm(w: PackedWeights, x: torch.Tensor, *, want_f32: bool = True, want
 
 
 # ------------------------------------------------------- 4-bit activations ----
+#
+# These calls take a few microseconds on the GPU for a single token, so the host
+# side counts: tensors are checked by their cheapest accessors, structs are packed
+# as bytes, and an operand's codes and scales share one allocation.
 
 _TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _FP4_FMTS = {"mxfp4": FMT_MXFP4, "nvfp4": FMT_NVFP4, FMT_MXFP4: FMT_MXFP4, FMT_NVFP4: FMT_NVFP4}
 _GATES = {"none": 0, "sigmoid": 1, "tanh": 2}
+_pack_fp4 = struct.Struct("@iiiPPP").pack                              # w4_fp4
+_pack_norm = struct.Struct("@iiiPPPPPqqqiiffffPqPqiiPPPP").pack        # w4_norm
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _fp4_fmt(fmt) -> int:
-    if fmt not in _FP4_FMTS:
+    f = _FP4_FMTS.get(fmt)
+    if f is None:
         raise ValueError("fmt must be 'mxfp4' or 'nvfp4'")
-    return _FP4_FMTS[fmt]
+    return f
 
 
 def _type(t: torch.Tensor, name: str) -> int:
-    if t.dtype not in _TYPES:
+    v = _TYPES.get(t.dtype)
+    if v is None:
         raise ValueError(f"{name} must be bfloat16, float16 or float32, got {t.dtype}")
-    return _TYPES[t.dtype]
+    return v
 
 
-def _same_device(ref: torch.Tensor, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != ref.device:
-            raise ValueError(f"{name} must be on {ref.device}, got {t.device}")
+def _new(rows: int, width: int, dtype, device) -> torch.Tensor:
+    """torch.empty((rows, width)), by the call that costs the host least."""
+    return torch.empty_strided((rows, width), (width, 1), dtype=dtype, device=device)
 
 
-def _rows(t: torch.Tensor, name: str, shape=None):
-    """(data pointer, row distance) of a 2-D CUDA tensor whose rows are contiguous."""
+def _rows(t: torch.Tensor, name: str, dev=None, rows=None, width=None):
+    """(data pointer, row distance, rows, width) of a 2-D CUDA tensor with contiguous
+    rows, on device `dev` and of the given shape where these are given."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (no CPU path)")
-    if t.dim() != 2 or (shape is not None and tuple(t.shape) != shape):
-        raise ValueError(f"{name} must have shape {shape or '[rows][K]'}, got {tuple(t.shape)}")
-    rows, width = t.shape
-    if width > 1 and t.stride(1) != 1:
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions, got {tuple(t.shape)}")
+    r, w = t.shape
+    if (rows is not None and (r != rows or w != width)) or (dev is not None and t.get_device() != dev):
+        raise ValueError(f"{name} must have shape {(rows, width)} on cuda:{dev}, got {(r, w)} on {t.device}")
+    s0, s1 = t.stride()
+    if s1 != 1 and w > 1:
         raise ValueError(f"{name} must have contiguous rows")
-    return t.data_ptr(), t.stride(0) if rows > 1 else width
+    return t.data_ptr(), s0 if r > 1 else w, r, w
 
 
-def _scalar(t: Optional[torch.Tensor], name: str, dtype):
-    """Data pointer of an optional one-element CUDA tensor."""
+def _vector(t: Optional[torch.Tensor], name: str, dtype, dev: int, n: int) -> int:
+    """Data pointer of an optional contiguous tensor of n values on device dev (0: none)."""
     if t is None:
-        return None
+        return 0
     _cuda(t, name, dtype)
-    if t.numel() != 1:
-        raise ValueError(f"{name} must hold one value")
+    if t.numel() != n or t.get_device() != dev:
+        raise ValueError(f"{name} must hold {n} values on cuda:{dev}, got {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
-def _call(device: torch.device, stream, what: str, fn, *args):
-    """fn(*args, stream) with `device` current; on its current stream when none is given."""
-    if device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            return _call(device, stream, what, fn, *args)
+def _call(dev: int, stream, what: str, fn, *args):
+    """fn(*args, stream) with device `dev` current; on its current stream when none is given."""
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return _call(dev, stream, what, fn, *args)
     if stream is not None:
         s = stream.cuda_stream
     else:
-        s = _raw_stream(device.index) if _raw_stream else torch.cuda.current_stream(device).cuda_stream
+        s = _raw_stream(dev) if _raw_stream else torch.cuda.current_stream(dev).cuda_stream
     status = fn(*args, s)
     if status:
         raise W4Error(status, what)
 
 
-@dataclass(frozen=True)
-class Fp4Tensor:
-    """A block-scaled 4-bit operand: rows x K values (w4_fp4 in include/w4a16.h).
-    Holds its tensors; the fields do not change after construction."""
-    fmt: int
-    rows: int
-    K: int
-    codes: torch.Tensor                    # uint8 [rows][K/2]
-    scales: torch.Tensor                   # uint8 [fp4_scale_bytes]: tiles of 128 rows x 4 scales
-    global_scale: Optional[torch.Tensor] = None   # float32 [1] (NVFP4)
+def fp4_scale_bytes(fmt: int, rows: int, K: int) -> int:
+    """Bytes of an operand's scale tiles (as fp4_scale_bytes in include/w4a16.h)."""
+    if fmt not in (FMT_MXFP4, FMT_NVFP4) or rows < 1 or K < 32 or K % 32:
+        return 0
+    return (rows + 127) // 128 * ((K + 127) // 128 if fmt == FMT_MXFP4 else (K + 63) // 64) * 512
 
-    def __post_init__(self):
-        _fp4_fmt(self.fmt)
-        _cuda(self.codes, "codes", torch.uint8)
-        _cuda(self.scales, "scales", torch.uint8)
-        if self.codes.numel() != self.rows * (self.K // 2):
+
+class Fp4Tensor:
+    """A block-scaled 4-bit operand of rows x K values (w4_fp4 in include/w4a16.h):
+
+        codes         uint8 [rows][K/2]
+        scales        uint8 [fp4_scale_bytes(fmt, rows, K)], tiles of 128 rows x 4 scales
+        global_scale  float32 [1] (NVFP4), None (MXFP4)
+
+    Holds its tensors; they do not change after construction."""
+    __slots__ = ("fmt", "rows", "K", "global_scale", "_codes", "_scales", "_buf", "_scales_at", "_codes_ptr",
+                 "_scales_ptr", "_gptr", "_c", "_dev", "device", "__weakref__")
+
+    def __init__(self, fmt: int, rows: int, K: int, codes: torch.Tensor, scales: torch.Tensor,
+                 global_scale: Optional[torch.Tensor] = None):
+        fmt = _fp4_fmt(fmt)
+        _cuda(codes, "codes", torch.uint8)
+        dev = codes.get_device()
+        n = fp4_scale_bytes(fmt, rows, K)
+        if not n:
+            raise W4Error(1, f"4-bit operand of {rows} x {K} (K % 32 == 0, one row at least)")
+        if codes.numel() != rows * (K // 2):
             raise ValueError("codes must hold rows * K / 2 bytes")
-        if self.scales.numel() != fp4_scale_bytes(self.fmt, self.rows, self.K):
-            raise ValueError("scales must hold fp4_scale_bytes(fmt, rows, K) bytes (K % 32 == 0)")
-        if (self.global_scale is None) != (self.fmt == FMT_MXFP4):
+        if (global_scale is None) != (fmt == FMT_MXFP4):
             raise ValueError("global_scale goes with NVFP4")
-        g = _scalar(self.global_scale, "global_scale", torch.float32)
-        _same_device(self.codes, scales=self.scales, global_scale=self.global_scale)
-        c = _Fp4(self.fmt, self.rows, self.K, self.codes.data_ptr(), self.scales.data_ptr(), g)
-        object.__setattr__(self, "_c", c)
-        object.__setattr__(self, "_ref", ctypes.byref(c))
+        self._scales_ptr = _vector(scales, "scales", torch.uint8, dev, n)
+        self._gptr = _vector(global_scale, "global_scale", torch.float32, dev, 1)
+        self.fmt, self.rows, self.K, self.global_scale = fmt, rows, K, global_scale
+        self._codes, self._scales, self._buf, self._dev, self.device = codes, scales, None, dev, codes.device
+        self._codes_ptr = codes.data_ptr()
+        self._c = _pack_fp4(fmt, rows, K, self._codes_ptr, self._scales_ptr, self._gptr)
+
+    @classmethod
+    def _empty(cls, fmt: int, rows: int, K: int, device: torch.device, dev: int, global_scale, gptr: int):
+        """A new operand whose codes and scales are two parts of one allocation."""
+        n = fp4_scale_bytes(fmt, rows, K)
+        if not n:
+            raise W4Error(1, f"4-bit operand of {rows} x {K} (K % 32 == 0, one row at least)")
+        at = (rows * (K // 2) + 255) & ~255
+        self = cls.__new__(cls)
+        self._buf = torch.empty_strided((at + n,), (1,), dtype=torch.uint8, device=device)
+        p = self._buf.data_ptr()
+        self.fmt, self.rows, self.K, self.global_scale = fmt, rows, K, global_scale
+        self._codes = self._scales = None
+        self._scales_at, self._codes_ptr, self._scales_ptr, self._gptr, self._dev = at, p, p + at, gptr, dev
+        self.device = device
+        self._c = _pack_fp4(fmt, rows, K, p, p + at, gptr)
+        return self
+
+    @property
+    def codes(self) -> torch.Tensor:
+        if self._codes is None:
+            self._codes = self._buf[:self.rows * (self.K // 2)].view(self.rows, self.K // 2)
+        return self._codes
+
+    @property
+    def scales(self) -> torch.Tensor:
+        if self._scales is None:
+            self._scales = self._buf[self._scales_at:]
+        return self._scales
 
     @property
     def nbytes(self) -> int:
-        return self.codes.numel() + self.scales.numel()
+        return self.rows * (self.K // 2) + fp4_scale_bytes(self.fmt, self.rows, self.K)
+
+    def __repr__(self) -> str:
+        name = "mxfp4" if self.fmt == FMT_MXFP4 else "nvfp4"
+        return f"Fp4Tensor({name}, rows={self.rows}, K={self.K}, device={self.device})"
 
 
-def fp4_scale_bytes(fmt: int, rows: int, K: int) -> int:
-    return lib().fp4_scale_bytes(fmt, rows, K)
-
-
-def _empty_fp4(fmt: int, rows: int, K: int, device, global_scale) -> Fp4Tensor:
-    if rows < 1 or K < 32 or K % 32:
-        raise W4Error(1, f"4-bit operand of {rows} x {K} (K % 32 == 0, one row at least)")
-    return Fp4Tensor(fmt, rows, K, torch.empty(rows, K // 2, dtype=torch.uint8, device=device),
-                     torch.empty(fp4_scale_bytes(fmt, rows, K), dtype=torch.uint8, device=device),
-                     global_scale if fmt == FMT_NVFP4 else None)
-
-
-def _check_out(out: Fp4Tensor, fmt: int, rows: int, K: int, global_scale):
-    if not isinstance(out, Fp4Tensor) or (out.fmt, out.rows, out.K) != (fmt, rows, K):
-        raise ValueError("out must be an Fp4Tensor of the result's format and shape")
-    if fmt == FMT_NVFP4 and global_scale is not None and out.global_scale.data_ptr() != global_scale.data_ptr():
+def _result(out: Optional[Fp4Tensor], fmt: int, rows: int, K: int, device, dev: int, global_scale) -> Fp4Tensor:
+    """The operand a quantiser writes: `out`, checked, or a new one."""
+    g = _vector(global_scale, "global_scale", torch.float32, dev, 1) if fmt == FMT_NVFP4 else 0
+    if out is None:
+        if fmt == FMT_NVFP4 and not g:
+            raise ValueError("nvfp4 needs a global_scale")
+        return Fp4Tensor._empty(fmt, rows, K, device, dev, global_scale if g else None, g)
+    if not isinstance(out, Fp4Tensor) or (out.fmt, out.rows, out.K, out._dev) != (fmt, rows, K, dev):
+        raise ValueError("out must be an Fp4Tensor of the result's format, shape and device")
+    if g and g != out._gptr:
         raise ValueError("out.global_scale must be the given global_scale")
     return out
 
@@ -499,20 +531,11 @@ def fp4_quantize(x: torch.Tensor, fmt="mxfp4", *, global_scale: Optional[torch.T
     """Quantise x[rows][K] (bf16, f16 or f32, K % 32 == 0) to "mxfp4" or, under a given
     global_scale (float32 [1]), "nvfp4" (see fp4_quantize in include/w4a16.h)."""
     fmt = _fp4_fmt(fmt)
-    ptr, ld = _rows(x, "x")
-    t = _type(x, "x")
-    rows, K = x.shape
-    g = _scalar(global_scale, "global_scale", torch.float32) if fmt == FMT_NVFP4 else None
-    if out is None:
-        if fmt == FMT_NVFP4 and g is None:
-            raise ValueError("nvfp4 needs a global_scale")
-        out = _empty_fp4(fmt, rows, K, x.device, global_scale)
-    else:
-        _check_out(out, fmt, rows, K, global_scale)
-    _same_device(x, out=out.codes, global_scale=out.global_scale, d_status=d_status)
-    c = out._c
-    _call(x.device, stream, "fp4_quantize", lib().fp4_quantize, ptr, t, ld, rows, K, fmt, scale_rule,
-          c.global_scale, c.codes, c.scales, _scalar(d_status, "d_status", torch.int32))
+    ptr, ld, rows, K = _rows(x, "x")
+    dev = x.get_device()
+    out = _result(out, fmt, rows, K, x.device, dev, global_scale)
+    _call(dev, stream, "fp4_quantize", lib().fp4_quantize, ptr, _type(x, "x"), ld, rows, K, fmt, scale_rule, out._gptr,
+          out._codes_ptr, out._scales_ptr, _vector(d_status, "d_status", torch.int32, dev, 1))
     return out
 
 
@@ -520,10 +543,9 @@ def fp4_dequantize(a: Fp4Tensor, dtype: torch.dtype = torch.bfloat16, *, out: Op
                    stream=None) -> torch.Tensor:
     """The values [rows][K] an operand stands for (see fp4_dequantize in include/w4a16.h)."""
     if out is None:
-        out = torch.empty(a.rows, a.K, dtype=dtype, device=a.codes.device)
-    ptr, ld = _rows(out, "out", (a.rows, a.K))
-    _same_device(a.codes, out=out)
-    _call(out.device, stream, "fp4_dequantize", lib().fp4_dequantize, a._ref, ptr, _type(out, "out"), ld)
+        out = _new(a.rows, a.K, dtype, a.device)
+    ptr, ld, _, _ = _rows(out, "out", a._dev, a.rows, a.K)
+    _call(a._dev, stream, "fp4_dequantize", lib().fp4_dequantize, a._c, ptr, _type(out, "out"), ld)
     return out
 
 
@@ -533,19 +555,13 @@ def fp4_from_rows(fmt, codes: torch.Tensor, row_scales: torch.Tensor, global_sca
     [rows][K/32] (MXFP4) or [rows][K/16] (NVFP4), which are laid out once."""
     fmt = _fp4_fmt(fmt)
     _cuda(codes, "codes", torch.uint8)
-    _cuda(row_scales, "row_scales", torch.uint8)
-    _same_device(codes, row_scales=row_scales, global_scale=global_scale)
     if codes.dim() != 2:
         raise ValueError("codes must have shape [rows][K/2]")
-    rows, K = codes.shape[0], 2 * codes.shape[1]
-    if tuple(row_scales.shape) != (rows, K // (32 if fmt == FMT_MXFP4 else 16)):
-        raise ValueError("row_scales do not match the codes")
-    if rows < 1 or K < 32 or K % 32:
-        raise W4Error(1, f"4-bit operand of {rows} x {K} (K % 32 == 0, one row at least)")
+    rows, K, dev = codes.shape[0], 2 * codes.shape[1], codes.get_device()
+    src = _vector(row_scales, "row_scales", torch.uint8, dev, rows * (K // (32 if fmt == FMT_MXFP4 else 16)))
     out = Fp4Tensor(fmt, rows, K, codes,
                     torch.empty(fp4_scale_bytes(fmt, rows, K), dtype=torch.uint8, device=codes.device), global_scale)
-    _call(codes.device, stream, "fp4_tile_scales", lib().fp4_tile_scales, fmt, rows, K, row_scales.data_ptr(),
-          out._c.scales)
+    _call(dev, stream, "fp4_tile_scales", lib().fp4_tile_scales, fmt, rows, K, src, out._scales_ptr)
     return out
 
 
@@ -557,29 +573,25 @@ def fp4_from_packed(w: PackedWeights, *, stream=None) -> Fp4Tensor:
     return fp4_from_rows(FMT_NVFP4, w.codes, w.scales, w.global_scale, stream=stream)
 
 
-def _product_out(w: Fp4Tensor, M: int, out_dtype, out: Optional[torch.Tensor], device):
-    if not isinstance(w, Fp4Tensor):
-        raise ValueError("w must be an Fp4Tensor (fp4_quantize, fp4_from_packed)")
-    if out is None:
-        out = torch.empty(M, w.rows, dtype=out_dtype, device=device)
-    ptr, ld = _rows(out, "out", (M, w.rows))
-    return out, ptr, ld, _type(out, "out")
-
-
 def w4a4_gemm(w: Fp4Tensor, x: Fp4Tensor, *, out_dtype: torch.dtype = torch.bfloat16,
               out: Optional[torch.Tensor] = None, flags: int = 0, stream=None) -> torch.Tensor:
     """y[M][N] = x_hat[M][K] . w_hat[N][K], both operands in 4 bits and of the same
     format; any M (see w4a4_gemm in include/w4a16.h)."""
-    if not isinstance(x, Fp4Tensor):
-        raise ValueError("x must be an Fp4Tensor (fp4_quantize, block_norm)")
-    out, ptr, ld, t = _product_out(w, x.rows, out_dtype, out, x.codes.device)
-    _same_device(out, w=w.codes, x=x.codes)
-    _call(out.device, stream, "w4a4_gemm", lib().w4a4_gemm, w._ref, x._ref, ptr, t, ld, flags)
+    if not isinstance(w, Fp4Tensor) or not isinstance(x, Fp4Tensor):
+        raise ValueError("w and x must be Fp4Tensor (fp4_quantize, fp4_from_packed, block_norm)")
+    dev = x._dev
+    if w._dev != dev:
+        raise ValueError(f"w must be on cuda:{dev}, got cuda:{w._dev}")
+    if out is None:
+        out = _new(x.rows, w.rows, out_dtype, x.device)
+    ptr, ld, _, _ = _rows(out, "out", dev, x.rows, w.rows)
+    _call(dev, stream, "w4a4_gemm", lib().w4a4_gemm, w._c, x._c, ptr, _type(out, "out"), ld, flags)
     return out
 
 
 def w4a4_workspace_bytes(w: Fp4Tensor, M: int) -> int:
-    return lib().w4a4_workspace_bytes(w._ref, M)
+    """Bytes of workspace w4a4_linear needs (as w4a4_workspace_bytes in include/w4a16.h)."""
+    return ((M * (w.K // 2) + 255) & ~255) + fp4_scale_bytes(w.fmt, M, w.K) if M >= 1 else 0
 
 
 def w4a4_linear(w: Fp4Tensor, x: torch.Tensor, *, global_scale: Optional[torch.Tensor] = None,
@@ -588,30 +600,28 @@ def w4a4_linear(w: Fp4Tensor, x: torch.Tensor, *, global_scale: Optional[torch.T
                 d_status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """y[M][N] = quantised x[M][K] . w_hat: fp4_quantize to w's format (under
     global_scale for NVFP4), then w4a4_gemm, in one call."""
-    ptr, ld = _rows(x, "x")
-    M, K = x.shape
-    out, yptr, yld, yt = _product_out(w, M, out_dtype, out, x.device)
+    if not isinstance(w, Fp4Tensor):
+        raise ValueError("w must be an Fp4Tensor (fp4_quantize, fp4_from_packed)")
+    dev = w._dev
+    ptr, ld, M, K = _rows(x, "x", dev)
     if K != w.K:
         raise ValueError(f"x has {K} columns, w {w.K}")
-    g = _scalar(global_scale, "global_scale", torch.float32) if w.fmt == FMT_NVFP4 else None
+    g = _vector(global_scale, "global_scale", torch.float32, dev, 1) if w.fmt == FMT_NVFP4 else 0
+    device = x.device
+    if out is None:
+        out = _new(M, w.rows, out_dtype, device)
+    yptr, yld, _, _ = _rows(out, "out", dev, M, w.rows)
     if workspace is None:
-        workspace = torch.empty(lib().w4a4_workspace_bytes(w._ref, M), dtype=torch.uint8, device=x.device)
+        need = w4a4_workspace_bytes(w, M)
+        workspace = torch.empty_strided((need,), (1,), dtype=torch.uint8, device=device)
     else:
         _cuda(workspace, "workspace", torch.uint8)
-    _same_device(x, w=w.codes, out=out, global_scale=global_scale, workspace=workspace, d_status=d_status)
-    _call(x.device, stream, "w4a4_linear", lib().w4a4_linear, w._ref, ptr, _type(x, "x"), ld, M, scale_rule, g,
-          yptr, yt, yld, workspace.data_ptr(), workspace.numel(), _scalar(d_status, "d_status", torch.int32))
+        need = workspace.numel()
+        if workspace.get_device() != dev:
+            raise ValueError(f"workspace must be on cuda:{dev}, got {workspace.device}")
+    _call(dev, stream, "w4a4_linear", lib().w4a4_linear, w._c, ptr, _type(x, "x"), ld, M, scale_rule, g, yptr,
+          _type(out, "out"), yld, workspace.data_ptr(), need, _vector(d_status, "d_status", torch.int32, dev, 1))
     return out
-
-
-def _width(t: Optional[torch.Tensor], name: str, D: int, dtype):
-    """Data pointer of an optional [D] tensor."""
-    if t is None:
-        return None
-    _cuda(t, name, dtype)
-    if tuple(t.shape) != (D,):
-        raise ValueError(f"{name} must have shape ({D},), got {tuple(t.shape)}")
-    return t.data_ptr()
 
 
 def block_norm(y: torch.Tensor, h: Optional[torch.Tensor] = None, *, post_weight: Optional[torch.Tensor] = None,
@@ -631,60 +641,56 @@ def block_norm(y: torch.Tensor, h: Optional[torch.Tensor] = None, *, post_weight
     if not given); gate_act "none", "sigmoid" or "tanh".  quantize "mxfp4" or "nvfp4"
     (under global_scale) gives z as an Fp4Tensor.  out_h may be h or y; want_h=False
     leaves h' out (None)."""
-    yp, ldy = _rows(y, "y")
-    t = _type(y, "y")
-    M, D = y.shape
-    dev = y.device
-    n = _Norm(type=t, M=M, D=D, y=yp, ldy=ldy, residual_scale=residual_scale, block_scale=block_scale, eps=eps,
-              weight_offset=weight_offset, scale_rule=scale_rule,
-              w_post=_width(post_weight, "post_weight", D, y.dtype), w_pre=_width(pre_weight, "pre_weight", D, y.dtype))
+    yp, ldy, M, D = _rows(y, "y")
+    dt, t, dev, device = y.dtype, _type(y, "y"), y.get_device(), y.device
+
+    def rows_of(v, name):
+        if v.dtype != dt:
+            raise ValueError(f"{name} must be {dt}, got {v.dtype}")
+        return _rows(v, name, dev, M, D)
+
+    hp = gp = ohp = zp = ldh = ldg = ldoh = ldz = 0
     if h is not None:
-        if h.dtype != y.dtype:
-            raise ValueError(f"h must be {y.dtype}, got {h.dtype}")
-        n.h, n.ldh = _rows(h, "h", (M, D))
-    if gate_act not in _GATES:
+        hp, ldh, _, _ = rows_of(h, "h")
+    act = _GATES.get(gate_act)
+    if act is None:
         raise ValueError("gate_act must be 'none', 'sigmoid' or 'tanh'")
-    if gate is not None:
-        g2 = gate.unsqueeze(0) if gate.dim() == 1 else gate
-        if g2.dtype != y.dtype:
-            raise ValueError(f"gate must be {y.dtype}, got {g2.dtype}")
-        G = g2.shape[0]
+    if gate is None:
+        gate_rows = 1
+    else:
+        if gate.dtype != dt:
+            raise ValueError(f"gate must be {dt}, got {gate.dtype}")
+        gp, ldg, G, gw = _rows(gate if gate.dim() == 2 else gate.unsqueeze(0), "gate", dev)
+        if gw != D:
+            raise ValueError(f"gate must have {D} columns, got {gw}")
         if gate_rows is None:
             if G < 1 or M % G:
                 raise ValueError(f"{G} gate rows do not divide {M} rows: give gate_rows")
             gate_rows = M // G
         if gate_rows < 1 or G * gate_rows < M:
             raise ValueError(f"{G} gate rows of {gate_rows} rows each do not cover {M} rows")
-        n.gate, n.ldgate = _rows(g2, "gate", (G, D))
-        n.gate_rows, n.gate_act = min(gate_rows, M), _GATES[gate_act]
-    if out_h is None and want_h:
-        out_h = torch.empty(M, D, dtype=y.dtype, device=dev)
+        gate_rows = min(gate_rows, M)
     if out_h is not None:
-        if out_h.dtype != y.dtype:
-            raise ValueError(f"out_h must be {y.dtype}, got {out_h.dtype}")
-        n.h_out, n.ldh_out = _rows(out_h, "out_h", (M, D))
+        ohp, ldoh, _, _ = rows_of(out_h, "out_h")
+    elif want_h:
+        out_h = _new(M, D, dt, device)
+        ohp, ldoh = out_h.data_ptr(), D
+    fmt = qg = qc = qs = qd = 0
     if quantize is None:
         if out is None:
-            out = torch.empty(M, D, dtype=y.dtype, device=dev)
-        if out.dtype != y.dtype:
-            raise ValueError(f"out must be {y.dtype}, got {out.dtype}")
-        n.z, n.ldz = _rows(out, "out", (M, D))
-        zdev = out
+            out = _new(M, D, dt, device)
+            zp, ldz = out.data_ptr(), D
+        else:
+            zp, ldz, _, _ = rows_of(out, "out")
     else:
         fmt = _fp4_fmt(quantize)
-        if out is None:
-            if fmt == FMT_NVFP4 and global_scale is None:
-                raise ValueError("nvfp4 needs a global_scale")
-            out = _empty_fp4(fmt, M, D, dev, global_scale)
-        else:
-            _check_out(out, fmt, M, D, global_scale)
-        c = out._c
-        n.quant_fmt, n.global_scale, n.codes, n.scales = fmt, c.global_scale, c.codes, c.scales
-        n.d_status = _scalar(d_status, "d_status", torch.int32)
-        zdev = out.codes
-    _same_device(y, h=h, gate=gate, post_weight=post_weight, pre_weight=pre_weight, out_h=out_h, out=zdev,
-                 global_scale=global_scale, d_status=d_status)
-    _call(dev, stream, "w4_block_norm", lib().w4_block_norm, ctypes.byref(n))
+        out = _result(out, fmt, M, D, device, dev, global_scale)
+        qg, qc, qs = out._gptr, out._codes_ptr, out._scales_ptr
+        qd = _vector(d_status, "d_status", torch.int32, dev, 1)
+    n = _pack_norm(t, M, D, yp, hp, _vector(post_weight, "post_weight", dt, dev, D),
+                   _vector(pre_weight, "pre_weight", dt, dev, D), gp, ldy, ldh, ldg, gate_rows, act, residual_scale,
+                   block_scale, eps, weight_offset, ohp, ldoh, zp, ldz, fmt, scale_rule, qg, qc, qs, qd)
+    _call(dev, stream, "w4_block_norm", lib().w4_block_norm, n)
     return out_h, out
 
 

@@ -12,7 +12,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 SRC_DIR = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libw4a16.so")
 MAIN = os.path.join(SRC_DIR, "w4a16.cu")
-UNITS = [MAIN, os.path.join(SRC_DIR, "noalloc.cu"), os.path.join(SRC_DIR, "fp4.cu")]
+UNITS = [MAIN] + [os.path.join(SRC_DIR, f) for f in ("noalloc.cu", "fp4.cu", "norm.cu")]
 
 NVCC_FLAGS = [
     "-O3", "-std=c++17", "-lineinfo",

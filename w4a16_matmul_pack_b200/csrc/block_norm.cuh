@@ -13,6 +13,8 @@
 // rounding of each output is its own.
 //
 // One CTA of at most MAXT threads per row, PV units of eight values per thread.
+// CTAs walk the rows: the weights (and a gate that serves every row) are loaded
+// once per CTA, and the next row's y is on its way while this row is reduced.
 #pragma once
 
 #include "fp4.cuh"
@@ -36,19 +38,10 @@ struct Args {
     const void *y, *h, *w_post, *w_pre, *gate;
     void *h_out, *z;
     long long ldy, ldh, ldgate, ldh_out, ldz;
-    int D, gate_rows, gate_act;
-    float residual_scale, block_scale, eps, offset;
+    int M, D, gate_rows, gate_act;
+    float inv_D, residual_scale, block_scale, eps, offset;
     fp4::Out q;   // 4-bit z
 };
-
-template <typename T> __device__ __forceinline__ float to_f32(T v);
-template <> __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
-template <> __device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
-template <> __device__ __forceinline__ float to_f32(float v) { return v; }
-template <typename T> __device__ __forceinline__ T from_f32(float v);
-template <> __device__ __forceinline__ __nv_bfloat16 from_f32(float v) { return __float2bfloat16_rn(v); }
-template <> __device__ __forceinline__ __half from_f32(float v) { return __float2half_rn(v); }
-template <> __device__ __forceinline__ float from_f32(float v) { return v; }
 
 template <int MODE>
 __device__ __forceinline__ int index(int p, int j) {
@@ -56,131 +49,266 @@ __device__ __forceinline__ int index(int p, int j) {
                            : 8 * (p * (int)blockDim.x + (int)threadIdx.x) + j;
 }
 
+// Eight values as they are stored.
+template <typename T> struct Raw { uint32_t w[2 * sizeof(T)]; };
+
+template <typename T> __device__ __forceinline__ void unpack(const Raw<T> &r, float2 (&v)[4]);
+template <> __device__ __forceinline__ void unpack<__nv_bfloat16>(const Raw<__nv_bfloat16> &r, float2 (&v)[4]) {
+#pragma unroll
+    for (int j = 0; j < 4; j++) v[j] = make_float2(bf16_lo(r.w[j]), bf16_hi(r.w[j]));
+}
+template <> __device__ __forceinline__ void unpack<__half>(const Raw<__half> &r, float2 (&v)[4]) {
+#pragma unroll
+    for (int j = 0; j < 4; j++) v[j] = __half22float2(*reinterpret_cast<const __half2 *>(&r.w[j]));
+}
+template <> __device__ __forceinline__ void unpack<float>(const Raw<float> &r, float2 (&v)[4]) {
+#pragma unroll
+    for (int j = 0; j < 4; j++) v[j] = make_float2(__uint_as_float(r.w[2 * j]), __uint_as_float(r.w[2 * j + 1]));
+}
+
+template <typename T> __device__ __forceinline__ void pack(const float2 (&v)[4], Raw<T> &r);
+template <> __device__ __forceinline__ void pack<__nv_bfloat16>(const float2 (&v)[4], Raw<__nv_bfloat16> &r) {
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        const __nv_bfloat162 b = __float22bfloat162_rn(v[j]);
+        r.w[j] = *reinterpret_cast<const uint32_t *>(&b);
+    }
+}
+template <> __device__ __forceinline__ void pack<__half>(const float2 (&v)[4], Raw<__half> &r) {
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        const __half2 b = __float22half2_rn(v[j]);
+        r.w[j] = *reinterpret_cast<const uint32_t *>(&b);
+    }
+}
+template <> __device__ __forceinline__ void pack<float>(const float2 (&v)[4], Raw<float> &r) {
+#pragma unroll
+    for (int j = 0; j < 4; j++) r.w[2 * j] = __float_as_uint(v[j].x), r.w[2 * j + 1] = __float_as_uint(v[j].y);
+}
+
+// A load that the compiler may move past stores: no output overlaps what is still to
+// be read (h_out may be h, z may be y, but every value is read before it is written,
+// by the same thread).  Zeros where it is not taken.
+__device__ __forceinline__ void load_if(bool take, const void *p, uint32_t *w) {
+    asm("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+        "@q ld.global.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
+        : "=&r"(w[0]), "=&r"(w[1]), "=&r"(w[2]), "=&r"(w[3]) : "l"(p), "r"((int)take));
+}
+
+// Unit p of a row; values past D are zero.
 template <typename T, int MODE>
-__device__ __forceinline__ void load_unit(const T *row, int p, int D, float (&v)[8]) {
+__device__ __forceinline__ void load_unit(const void *base, long long offset, int p, int D, Raw<T> &r) {
+    const T *row = reinterpret_cast<const T *>(base) + offset;
+    constexpr int WORDS = 2 * sizeof(T);
     if constexpr (MODE == VECTOR) {
         const int i = index<MODE>(p, 0);
-        uint32_t unused;
-        if (i < D) {
-            fp4::load8<T>(row + i, v, unused);
-        } else {
 #pragma unroll
-            for (int j = 0; j < 8; j++) v[j] = 0.0f;
-        }
+        for (int q = 0; q < WORDS; q += 4) load_if(i < D, reinterpret_cast<const uint32_t *>(row + i) + q, r.w + q);
     } else {
 #pragma unroll
         for (int j = 0; j < 8; j++) {
             const int i = index<MODE>(p, j);
-            v[j] = i < D ? to_f32<T>(row[i]) : 0.0f;
+            if constexpr (sizeof(T) == 4) {
+                r.w[j] = i < D ? reinterpret_cast<const uint32_t *>(row)[i] : 0u;
+            } else {
+                const uint32_t u = i < D ? reinterpret_cast<const uint16_t *>(row)[i] : 0u;
+                r.w[j / 2] = j % 2 ? r.w[j / 2] | (u << 16) : u;
+            }
         }
     }
 }
 
 template <typename T, int MODE>
-__device__ __forceinline__ void store_row_unit(T *row, int p, int D, const float (&v)[8]) {
+__device__ __forceinline__ Raw<T> fresh_unit(const void *base, long long offset, int p, int D) {
+    Raw<T> r;
+    load_unit<T, MODE>(base, offset, p, D, r);
+    return r;
+}
+
+template <typename T, int MODE>
+__device__ __forceinline__ void store_unit(void *base, long long offset, int p, int D, const float2 (&v)[4]) {
+    T *row = reinterpret_cast<T *>(base) + offset;
+    constexpr int WORDS = 2 * sizeof(T);
+    Raw<T> r;
+    pack<T>(v, r);
     if constexpr (MODE == VECTOR) {
         const int i = index<MODE>(p, 0);
-        if (i < D) fp4::store8(row + i, v);
+        if (i < D)
+#pragma unroll
+            for (int q = 0; q < WORDS / 4; q++)
+                reinterpret_cast<uint4 *>(row + i)[q] =
+                    make_uint4(r.w[4 * q], r.w[4 * q + 1], r.w[4 * q + 2], r.w[4 * q + 3]);
     } else {
 #pragma unroll
         for (int j = 0; j < 8; j++) {
             const int i = index<MODE>(p, j);
-            if (i < D) row[i] = from_f32<T>(v[j]);
+            if (i >= D) continue;
+            if constexpr (sizeof(T) == 4) reinterpret_cast<uint32_t *>(row)[i] = r.w[j];
+            else reinterpret_cast<uint16_t *>(row)[i] = (uint16_t)(r.w[j / 2] >> (16 * (j % 2)));
         }
     }
 }
 
-// Sum over the CTA; every thread gets the same value.
+// Sum over the CTA; every thread gets the same value.  part: 32 floats, zero past
+// the CTA's warps, free of readers since the last barrier but one.
 __device__ __forceinline__ float block_sum(float s, float *part) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-    const int warps = blockDim.x >> 5;
-    if (warps == 1) return s;
+    if (blockDim.x == 32) return s;
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = s;
     __syncthreads();
     float t = 0.0f;
-    for (int w = 0; w < warps; w++) t += part[w];
+    for (int w = 0; w < (int)(blockDim.x >> 5); w += 4) {
+        const float4 f = *reinterpret_cast<const float4 *>(part + w);
+        t += (f.x + f.y) + (f.z + f.w);
+    }
     return t;
 }
 
-__device__ __forceinline__ float gate_value(float g, int act) {
-    if (act == GATE_SIGMOID) return 1.0f / (1.0f + expf(-g));
-    if (act == GATE_TANH) return tanhf(g);
-    return g;
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+
+// act(gate).
+//   sigmoid: 1 / (1 + 2^(-g log2 e)); the argument's rounding costs |g| 2^-24, the
+//   exponential and the division 2^-22 each.
+//   tanh: from 0.3 on 1 - 2 / (1 + 2^(2 g log2 e)) (what the subtraction loses is at most
+//   two bits there); below, its Taylor series to g^9 (the next term is 5e-8 of the sum).
+// The library's tanhf inlined for every value of a row is code enough to make the
+// kernel wait for instructions.
+__device__ __forceinline__ float act_value(float g, int act) {
+    if (act == GATE_SIGMOID) return __fdividef(1.0f, 1.0f + exp2f(-1.44269504f * g));
+    const float s = g * g, x = fabsf(g);
+    const float big = copysignf(1.0f - __fdividef(2.0f, 1.0f + exp2f(2.88539008f * x)), g);
+    const float small = fmaf(g * s, fmaf(s, fmaf(s, fmaf(s, 62.0f / 2835.0f, -17.0f / 315.0f), 2.0f / 15.0f),
+                                         -1.0f / 3.0f), g);
+    return x < 0.3f ? small : big;
+}
+template <bool ACT>
+__device__ __forceinline__ void apply_gate(float2 (&v)[4], const float2 (&g)[4], int act) {
+#pragma unroll
+    for (int j = 0; j < 4; j++)
+        v[j] = __fmul2_rn(v[j], ACT ? make_float2(act_value(g[j].x, act), act_value(g[j].y, act)) : g[j]);
 }
 
-// QFMT 0: z in T; else z in that 4-bit format.
-template <typename T, int PV, int MAXT, int MODE, int QFMT>
-__global__ void __launch_bounds__(MAXT) block_norm_kernel(const Args a) {
-    __shared__ float part[2][32];
+// v *= w + offset
+template <typename T>
+__device__ __forceinline__ void apply_weight(const Raw<T> &r, float offset, float2 (&v)[4]) {
+    float2 w[4];
+    unpack<T>(r, w);
+#pragma unroll
+    for (int j = 0; j < 4; j++) v[j] = __fmul2_rn(v[j], __fadd2_rn(w[j], both(offset)));
+}
+
+// QFMT 0: z in T; else z in that 4-bit format.  ACT: the gate goes through sigmoid or
+// tanh.  KEEP: the weights (and a gate that
+// serves every row) stay in registers from row to row, as they are stored, and the
+// next row is loaded ahead; without it (wide rows, which take the registers for
+// themselves) everything is loaded where it is used.
+//
+// At 21 M values in 26 us (8192 x 2560 BF16 at the copy rate) an SM lane has 45
+// issue slots per value, and this kernel takes about 40 of them (36.5 us, 71% of the
+// slots used): the arithmetic is in pairs (f32x2) and weights and gate stay packed.
+// Measured slower there: two units per thread (fewer instructions, but fewer warps:
+// 47 us); no row ahead and twice the CTAs (42 us); one warp per row without barriers
+// (its unrolled row is code run once per row, and the warps wait for instructions:
+// 47 us).
+template <typename T, int PV, int MAXT, int MINB, bool KEEP, int MODE, int QFMT, bool ACT>
+__global__ void __launch_bounds__(MAXT, MINB) block_norm_kernel(const __grid_constant__ Args a) {
+    __shared__ __align__(16) float part[4][32];
     pdl_allow_dependents();
-    const long long m = blockIdx.x;
     const int D = a.D;
-    float b[PV][8];
-    const T *yr = reinterpret_cast<const T *>(a.y) + m * a.ldy;
-    float ss = 0.0f;
+    constexpr int KV = KEEP ? PV : 1;
+    Raw<T> y[PV], h[KV], g[KV], w_post[KV], w_pre[KV];
+    int m = blockIdx.x;
+    const bool one_gate = a.gate_rows >= a.M;
+    const float qg = QFMT == W4_FMT_NVFP4 ? __ldg(a.q.global_scale) : 1.0f;
 #pragma unroll
-    for (int p = 0; p < PV; p++) load_unit<T, MODE>(yr, p, D, b[p]);
-    float hv[PV][8];
-    const T *hr = reinterpret_cast<const T *>(a.h) + m * a.ldh;
-    if (a.h) {
-#pragma unroll
-        for (int p = 0; p < PV; p++) load_unit<T, MODE>(hr, p, D, hv[p]);
-    }
-    if (a.w_post) {
-#pragma unroll
-        for (int p = 0; p < PV; p++)
-#pragma unroll
-            for (int j = 0; j < 8; j++) ss = fmaf(b[p][j], b[p][j], ss);
-        const float r = rsqrtf(block_sum(ss, part[0]) / (float)D + a.eps);
+    for (int p = 0; p < PV; p++) load_unit<T, MODE>(a.y, m * a.ldy, p, D, y[p]);
+    if constexpr (KEEP) {
 #pragma unroll
         for (int p = 0; p < PV; p++) {
-            float w[8];
-            load_unit<T, MODE>(reinterpret_cast<const T *>(a.w_post), p, D, w);
-#pragma unroll
-            for (int j = 0; j < 8; j++) b[p][j] = b[p][j] * r * (w[j] + a.offset);
+            if (a.h) load_unit<T, MODE>(a.h, m * a.ldh, p, D, h[p]);
+            if (a.gate) load_unit<T, MODE>(a.gate, (m / a.gate_rows) * a.ldgate, p, D, g[p]);
         }
-    }
-    if (a.gate) {
-        const T *gr = reinterpret_cast<const T *>(a.gate) + (m / a.gate_rows) * a.ldgate;
 #pragma unroll
         for (int p = 0; p < PV; p++) {
-            float g[8];
-            load_unit<T, MODE>(gr, p, D, g);
-#pragma unroll
-            for (int j = 0; j < 8; j++) b[p][j] *= gate_value(g[j], a.gate_act);
+            if (a.w_post) load_unit<T, MODE>(a.w_post, 0, p, D, w_post[p]);
+            if (a.w_pre) load_unit<T, MODE>(a.w_pre, 0, p, D, w_pre[p]);
         }
     }
-    ss = 0.0f;
+    for (int i = threadIdx.x; i < 128; i += blockDim.x) part[i >> 5][i & 31] = 0.0f;
+    __syncthreads();
+    for (int row = 0;; row++) {
+        float *sums = part[2 * (row & 1)];
+        const int next = m + (int)gridDim.x;
+        float2 b[PV][4];
+        float2 ss = make_float2(0.0f, 0.0f);
 #pragma unroll
-    for (int p = 0; p < PV; p++)
-#pragma unroll
-        for (int j = 0; j < 8; j++) {
-            // values past D are zero in b and hv, so they add nothing
-            b[p][j] = a.h ? fmaf(a.residual_scale, hv[p][j], a.block_scale * b[p][j]) : a.block_scale * b[p][j];
-            ss = fmaf(b[p][j], b[p][j], ss);
+        for (int p = 0; p < PV; p++) {
+            unpack<T>(y[p], b[p]);
+            if (KEEP && next < a.M) load_unit<T, MODE>(a.y, next * a.ldy, p, D, y[p]);
         }
-    if (a.h_out) {
-        T *ho = reinterpret_cast<T *>(a.h_out) + m * a.ldh_out;
+        float scale = a.block_scale;
+        if (a.w_post) {
 #pragma unroll
-        for (int p = 0; p < PV; p++) store_row_unit<T, MODE>(ho, p, D, b[p]);
-    }
-    const float r = rsqrtf(block_sum(ss, part[1]) / (float)D + a.eps);
-    const float g = QFMT == W4_FMT_NVFP4 ? __ldg(a.q.global_scale) : 1.0f;
+            for (int p = 0; p < PV; p++)
 #pragma unroll
-    for (int p = 0; p < PV; p++) {
-        float w[8];
-        if (a.w_pre) load_unit<T, MODE>(reinterpret_cast<const T *>(a.w_pre), p, D, w);
-#pragma unroll
-        for (int j = 0; j < 8; j++) b[p][j] = a.w_pre ? b[p][j] * r * (w[j] + a.offset) : b[p][j] * r;
-        if constexpr (QFMT == 0) {
-            store_row_unit<T, MODE>(reinterpret_cast<T *>(a.z) + m * a.ldz, p, D, b[p]);
-        } else {
-            const int u = p * (int)blockDim.x + (int)threadIdx.x;
-            const bool active = u < D / fp4::kUnit;
-            // past D: 0 * r may be NaN (r of a row with Inf); the padding stays zero
-            fp4::store_unit<QFMT>(a.q, (int)m, u, active, b[p], active ? fp4::absmax_bits(b[p]) : 0u, g);
+                for (int j = 0; j < 4; j++) ss = __ffma2_rn(b[p][j], b[p][j], ss);
+            scale *= rsqrtf(block_sum(ss.x + ss.y, sums) * a.inv_D + a.eps);
+            ss = make_float2(0.0f, 0.0f);
         }
+        const float2 scale2 = both(scale), res2 = both(a.residual_scale);
+#pragma unroll
+        for (int p = 0; p < PV; p++) {
+            const int k = KEEP ? p : 0;
+#pragma unroll
+            for (int j = 0; j < 4; j++) b[p][j] = __fmul2_rn(b[p][j], scale2);
+            if (a.w_post) {
+                apply_weight<T>(KEEP ? w_post[k] : fresh_unit<T, MODE>(a.w_post, 0, p, D), a.offset, b[p]);
+            }
+            if (a.gate) {
+                float2 v[4];
+                unpack<T>(KEEP ? g[k] : fresh_unit<T, MODE>(a.gate, (m / a.gate_rows) * a.ldgate, p, D), v);
+                if (KEEP && !one_gate && next < a.M)
+                    load_unit<T, MODE>(a.gate, (next / a.gate_rows) * a.ldgate, p, D, g[p]);
+                apply_gate<ACT>(b[p], v, a.gate_act);
+            }
+            if (a.h) {
+                float2 v[4];
+                unpack<T>(KEEP ? h[k] : fresh_unit<T, MODE>(a.h, m * a.ldh, p, D), v);
+                if (KEEP && next < a.M) load_unit<T, MODE>(a.h, next * a.ldh, p, D, h[p]);
+#pragma unroll
+                for (int j = 0; j < 4; j++) b[p][j] = __ffma2_rn(res2, v[j], b[p][j]);
+            }
+            // values past D are zero in b and v, so they add nothing
+#pragma unroll
+            for (int j = 0; j < 4; j++) ss = __ffma2_rn(b[p][j], b[p][j], ss);
+            if (a.h_out) store_unit<T, MODE>(a.h_out, m * a.ldh_out, p, D, b[p]);
+        }
+        const float2 r = both(rsqrtf(block_sum(ss.x + ss.y, sums + 32) * a.inv_D + a.eps));
+#pragma unroll
+        for (int p = 0; p < PV; p++) {
+#pragma unroll
+            for (int j = 0; j < 4; j++) b[p][j] = __fmul2_rn(b[p][j], r);
+            if (a.w_pre) {
+                apply_weight<T>(KEEP ? w_pre[KEEP ? p : 0] : fresh_unit<T, MODE>(a.w_pre, 0, p, D), a.offset, b[p]);
+            }
+            if constexpr (QFMT == 0) {
+                store_unit<T, MODE>(a.z, m * a.ldz, p, D, b[p]);
+            } else {
+                const int u = p * (int)blockDim.x + (int)threadIdx.x;
+                const bool active = u < D / fp4::kUnit;
+                const float v[8] = {b[p][0].x, b[p][0].y, b[p][1].x, b[p][1].y,
+                                    b[p][2].x, b[p][2].y, b[p][3].x, b[p][3].y};
+                // past D: 0 * r may be NaN (r of a row with Inf); the padding stays zero
+                fp4::store_unit<QFMT>(a.q, m, u, active, v, active ? fp4::absmax_bits(v) : 0u, qg);
+            }
+        }
+        if (next >= a.M) break;
+        m = next;
+        if (!KEEP)
+#pragma unroll
+            for (int p = 0; p < PV; p++) load_unit<T, MODE>(a.y, m * a.ldy, p, D, y[p]);
     }
 }
 

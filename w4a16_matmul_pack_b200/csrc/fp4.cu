@@ -1,15 +1,14 @@
 // fp4.cu -- the W4A4 part of the C ABI (declared in include/w4a16.h): host-side
 // validation, launch configuration and launches of the sm_100a kernels that
-// quantise activations to 4 bits, multiply two 4-bit operands, and run the
-// norms, gate and residual between two such products.
+// quantise activations to 4 bits and multiply two 4-bit operands.
 #include <cuda_runtime.h>
 
 #include <stdlib.h>
 
 #include <algorithm>
 
-#include "block_norm.cuh"
-#include "fp4.cuh"
+#include "fp4_host.cuh"
+#include "fp4_pack.cuh"
 #include "fp4_gemm.cuh"
 #include "fp4_skinny.cuh"
 
@@ -17,14 +16,15 @@ using namespace w4;
 
 namespace w4 {
 
-// The sticky error word and the wait limit of this file's kernels are its own
-// copies (one per translation unit); w4_device_error and w4_set_wait_limit act on
-// both through these.
+int norm_device_error(int *out, int clear);   // norm.cu
+
+// The sticky error word and the wait limit are one copy per translation unit;
+// w4_device_error and w4_set_wait_limit act on those of the W4A4 kernels through
+// these.
 int fp4_device_error(int *out, int clear) {
-    if (cudaMemcpyFromSymbol(out, g_device_error, sizeof(int)) != cudaSuccess) return W4_ERR_CUDA;
-    const int zero = 0;
-    if (clear && cudaMemcpyToSymbol(g_device_error, &zero, sizeof(int)) != cudaSuccess) return W4_ERR_CUDA;
-    return W4_OK;
+    *out = 0;
+    const w4_status s = take_device_error(out, clear);
+    return s != W4_OK ? s : norm_device_error(out, clear);
 }
 
 int fp4_set_wait_limit(unsigned long long ns) {
@@ -35,96 +35,60 @@ int fp4_set_wait_limit(unsigned long long ns) {
 
 namespace {
 
-inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-inline bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-inline cudaStream_t as_stream(void *s) { return reinterpret_cast<cudaStream_t>(s); }
-inline w4_status launch_status() { return cudaGetLastError() == cudaSuccess ? W4_OK : W4_ERR_CUDA; }
-
-inline bool is_fp4(int fmt) { return fmt == W4_FMT_MXFP4 || fmt == W4_FMT_NVFP4; }
-inline int type_size(int type) { return type == W4_TYPE_F32 ? 4 : 2; }
-inline bool is_type(int type) { return type == W4_TYPE_BF16 || type == W4_TYPE_F16 || type == W4_TYPE_F32; }
-// Rows of `ld` values of `type` that all start on 16 bytes.
-inline bool rows16(long long ld, int type) { return ld * type_size(type) % 16 == 0; }
-
-constexpr long long kMaxBlocks = 0x7FFFFFFFll;
-
-w4_status device_sms(int &sms) {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return W4_ERR_CUDA;
-    return W4_OK;
+// Lanes of a pass over a matrix, 32 values each, rows padded to whole scale words.
+template <typename F>
+w4_status by_lanes(int rows, int K, F launch) {
+    const int per_row = (K / 32 + 3) / 4 * 4;
+    const long long blocks = ((long long)rows * per_row + 255) / 256;
+    if (blocks > kMaxBlocks) return W4_ERR_UNSUPPORTED;
+    launch((unsigned)blocks, per_row);
+    return launch_status();
 }
 
-w4_status check_operand(const w4_fp4 *a) {
-    if (!a || !is_fp4(a->fmt) || a->rows < 1 || a->K < 32 || a->K % 32 || !a->codes || !a->scales) return W4_ERR_ARG;
-    if (a->fmt == W4_FMT_NVFP4 && !a->global_scale) return W4_ERR_ARG;
-    if (!aligned16(a->codes) || !aligned16(a->scales) || !aligned4(a->global_scale)) return W4_ERR_ALIGN;
-    return W4_OK;
-}
-
-// A quantiser's output side.
-w4_status check_quantised(int rows, int K, int fmt, int scale_rule, const float *global_scale, const uint8_t *codes,
-                          const uint8_t *scales, const int *d_status) {
-    if (!is_fp4(fmt) || rows < 1 || K < 32 || K % 32 || !codes || !scales) return W4_ERR_ARG;
-    if (scale_rule != W4_MX_SCALE_FLOOR && scale_rule != W4_MX_SCALE_CEIL) return W4_ERR_ARG;
-    if (fmt == W4_FMT_NVFP4 && (!global_scale || scale_rule != W4_MX_SCALE_FLOOR)) return W4_ERR_ARG;
-    if (!aligned16(codes) || !aligned16(scales) || !aligned4(global_scale) || !aligned4(d_status)) return W4_ERR_ALIGN;
-    return W4_OK;
-}
-
-fp4::Out quantised_out(int K, int fmt, int scale_rule, const float *global_scale, uint8_t *codes, uint8_t *scales,
-                       int *d_status) {
-    fp4::Out o;
-    o.codes = codes;
-    o.scales = scales;
-    o.global_scale = global_scale;
-    o.d_status = d_status;
-    o.K = K;
-    o.tiles_k = fp4::scale_tiles_k(fmt, K);
-    o.ceil_rule = scale_rule == W4_MX_SCALE_CEIL;
-    return o;
-}
-
-w4_status clear_status(int *d_status, cudaStream_t st) {
-    return !d_status || cudaMemsetAsync(d_status, 0, sizeof(int), st) == cudaSuccess ? W4_OK : W4_ERR_CUDA;
+template <typename T, int FMT>
+w4_status launch_quantize(const void *x, long long ldx, int rows, const fp4::Out &o, cudaStream_t st) {
+    const T *p = reinterpret_cast<const T *>(x);
+    const bool wide = (reinterpret_cast<uintptr_t>(x) | (uintptr_t)(ldx * sizeof(T))) % 32 == 0;
+    return by_lanes(rows, o.K, [&](unsigned blocks, int per_row) {
+        if (wide) fp4::quantize_kernel<T, FMT, true><<<blocks, 256, 0, st>>>(p, ldx, rows, per_row, o);
+        else fp4::quantize_kernel<T, FMT, false><<<blocks, 256, 0, st>>>(p, ldx, rows, per_row, o);
+    });
 }
 
 template <typename T>
-w4_status launch_quantize(const void *x, long long ldx, int rows, int fmt, const fp4::Out &o, cudaStream_t st) {
-    const int pieces = (o.K / fp4::kUnit + 31) / 32;
-    const long long blocks = ((long long)rows * pieces + 7) / 8;
-    if (blocks > kMaxBlocks) return W4_ERR_UNSUPPORTED;
-    if (fmt == W4_FMT_MXFP4)
-        fp4::quantize_kernel<T, W4_FMT_MXFP4>
-            <<<(unsigned)blocks, 256, 0, st>>>(reinterpret_cast<const T *>(x), ldx, rows, pieces, o);
-    else
-        fp4::quantize_kernel<T, W4_FMT_NVFP4>
-            <<<(unsigned)blocks, 256, 0, st>>>(reinterpret_cast<const T *>(x), ldx, rows, pieces, o);
-    return launch_status();
+w4_status launch_quantize_fmt(const void *x, long long ldx, int rows, int fmt, const fp4::Out &o, cudaStream_t st) {
+    return fmt == W4_FMT_MXFP4 ? launch_quantize<T, W4_FMT_MXFP4>(x, ldx, rows, o, st)
+                               : launch_quantize<T, W4_FMT_NVFP4>(x, ldx, rows, o, st);
 }
 
 w4_status quantize(const void *x, int type, long long ldx, int rows, int fmt, const fp4::Out &o, cudaStream_t st) {
     switch (type) {
-    case W4_TYPE_BF16: return launch_quantize<__nv_bfloat16>(x, ldx, rows, fmt, o, st);
-    case W4_TYPE_F16: return launch_quantize<__half>(x, ldx, rows, fmt, o, st);
-    case W4_TYPE_F32: return launch_quantize<float>(x, ldx, rows, fmt, o, st);
+    case W4_TYPE_BF16: return launch_quantize_fmt<__nv_bfloat16>(x, ldx, rows, fmt, o, st);
+    case W4_TYPE_F16: return launch_quantize_fmt<__half>(x, ldx, rows, fmt, o, st);
+    case W4_TYPE_F32: return launch_quantize_fmt<float>(x, ldx, rows, fmt, o, st);
     }
     return W4_ERR_ARG;
 }
 
-template <typename T>
+template <typename T, int FMT>
 w4_status launch_dequantize(const w4_fp4 *a, void *out, long long ldo, cudaStream_t st) {
-    const int pieces = (a->K / fp4::kUnit + 31) / 32, tiles_k = fp4::scale_tiles_k(a->fmt, a->K);
-    const long long blocks = ((long long)a->rows * pieces + 7) / 8;
-    if (blocks > kMaxBlocks) return W4_ERR_UNSUPPORTED;
-    if (a->fmt == W4_FMT_MXFP4)
-        fp4::dequantize_kernel<T, W4_FMT_MXFP4><<<(unsigned)blocks, 256, 0, st>>>(
-            a->codes, a->scales, a->global_scale, a->rows, a->K, tiles_k, pieces, reinterpret_cast<T *>(out), ldo);
-    else
-        fp4::dequantize_kernel<T, W4_FMT_NVFP4><<<(unsigned)blocks, 256, 0, st>>>(
-            a->codes, a->scales, a->global_scale, a->rows, a->K, tiles_k, pieces, reinterpret_cast<T *>(out), ldo);
-    return launch_status();
+    T *p = reinterpret_cast<T *>(out);
+    const int tiles_k = fp4::scale_tiles_k(FMT, a->K);
+    const bool wide = (reinterpret_cast<uintptr_t>(out) | (uintptr_t)(ldo * sizeof(T))) % 32 == 0;
+    return by_lanes(a->rows, a->K, [&](unsigned blocks, int per_row) {
+        if (wide)
+            fp4::dequantize_kernel<T, FMT, true><<<blocks, 256, 0, st>>>(a->codes, a->scales, a->global_scale, a->rows,
+                                                                         a->K, tiles_k, per_row, p, ldo);
+        else
+            fp4::dequantize_kernel<T, FMT, false><<<blocks, 256, 0, st>>>(a->codes, a->scales, a->global_scale,
+                                                                          a->rows, a->K, tiles_k, per_row, p, ldo);
+    });
+}
+
+template <typename T>
+w4_status launch_dequantize_fmt(const w4_fp4 *a, void *out, long long ldo, cudaStream_t st) {
+    return a->fmt == W4_FMT_MXFP4 ? launch_dequantize<T, W4_FMT_MXFP4>(a, out, ldo, st)
+                                  : launch_dequantize<T, W4_FMT_NVFP4>(a, out, ldo, st);
 }
 
 // ------------------------------------------------------------------ product --
@@ -301,36 +265,6 @@ w4_status product(const w4_fp4 *w, const w4_fp4 *x, void *y, long long ldy, int 
 // Codes first, then scales on the next 256 bytes.
 size_t linear_scales_at(int rows, int K) { return ((size_t)rows * (K / 2) + 255) & ~(size_t)255; }
 
-// -------------------------------------------------------------------- norms --
-
-template <typename T, int PV, int MAXT, int QFMT>
-void launch_norm_mode(const norm::Args &a, int mode, int M, int threads, cudaStream_t st) {
-    if (mode == norm::VECTOR)
-        norm::block_norm_kernel<T, PV, MAXT, norm::VECTOR, QFMT><<<M, threads, 0, st>>>(a);
-    else if constexpr (QFMT != 0)
-        norm::block_norm_kernel<T, PV, MAXT, norm::SCALAR, QFMT><<<M, threads, 0, st>>>(a);
-    else
-        norm::block_norm_kernel<T, PV, MAXT, norm::STRIDED, QFMT><<<M, threads, 0, st>>>(a);
-}
-
-template <typename T, int QFMT>
-w4_status launch_norm(const norm::Args &a, int mode, int M, cudaStream_t st) {
-    const int units = (a.D + fp4::kUnit - 1) / fp4::kUnit;
-    auto threads = [&](int pv) { return ((units + pv - 1) / pv + 31) / 32 * 32; };
-    if (units <= 512) launch_norm_mode<T, 1, 512, QFMT>(a, mode, M, threads(1), st);
-    else if (units <= 1024) launch_norm_mode<T, 2, 512, QFMT>(a, mode, M, threads(2), st);
-    else if (units <= 2048) launch_norm_mode<T, 4, 512, QFMT>(a, mode, M, threads(4), st);
-    else launch_norm_mode<T, 4, 1024, QFMT>(a, mode, M, threads(4), st);
-    return launch_status();
-}
-
-template <typename T>
-w4_status launch_norm_fmt(const norm::Args &a, int mode, int M, int fmt, cudaStream_t st) {
-    if (fmt == 0) return launch_norm<T, 0>(a, mode, M, st);
-    if (fmt == W4_FMT_MXFP4) return launch_norm<T, W4_FMT_MXFP4>(a, mode, M, st);
-    return launch_norm<T, W4_FMT_NVFP4>(a, mode, M, st);
-}
-
 }  // namespace
 
 // ======================================================================== ABI
@@ -360,9 +294,9 @@ w4_status fp4_dequantize(const w4_fp4 *a, void *out, int type, long long ldo, vo
     if (!out || !is_type(type) || ldo < a->K) return W4_ERR_ARG;
     if (!aligned16(out) || !rows16(ldo, type)) return W4_ERR_ALIGN;
     cudaStream_t st = as_stream(stream);
-    if (type == W4_TYPE_BF16) return launch_dequantize<__nv_bfloat16>(a, out, ldo, st);
-    if (type == W4_TYPE_F16) return launch_dequantize<__half>(a, out, ldo, st);
-    return launch_dequantize<float>(a, out, ldo, st);
+    if (type == W4_TYPE_BF16) return launch_dequantize_fmt<__nv_bfloat16>(a, out, ldo, st);
+    if (type == W4_TYPE_F16) return launch_dequantize_fmt<__half>(a, out, ldo, st);
+    return launch_dequantize_fmt<float>(a, out, ldo, st);
 }
 
 w4_status fp4_tile_scales(int fmt, int rows, int K, const uint8_t *row_scales, uint8_t *scales, void *stream) {
@@ -408,48 +342,6 @@ w4_status w4a4_linear(const w4_fp4 *w, const void *x, int type, long long ldx, i
     if (s != W4_OK) return s;
     // the kernel just launched does not write the weights
     return product(w, &q, y, ldy, out_type, true, st);
-}
-
-w4_status w4_block_norm(const w4_norm *n, void *stream) {
-    if (!n || !n->y || n->M < 1 || n->D < 1 || !is_type(n->type) || !(n->eps >= 0.0f)) return W4_ERR_ARG;
-    if (n->D > norm::kMaxD) return W4_ERR_UNSUPPORTED;
-    if (n->ldy < n->D || (n->h && n->ldh < n->D) || (n->h_out && n->ldh_out < n->D)) return W4_ERR_ARG;
-    if (n->gate && (n->gate_rows < 1 || n->ldgate < n->D)) return W4_ERR_ARG;
-    if (n->gate_act < W4_GATE_NONE || n->gate_act > W4_GATE_TANH) return W4_ERR_ARG;
-    const int size = type_size(n->type);
-    auto on = [&](const void *p, int bytes) { return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(bytes - 1)) == 0; };
-    const void *ptrs[] = {n->y, n->h, n->w_post, n->w_pre, n->gate, n->h_out, n->z};
-    bool vec = n->D % fp4::kUnit == 0 && rows16(n->ldy, n->type) && (!n->h || rows16(n->ldh, n->type)) &&
-               (!n->h_out || rows16(n->ldh_out, n->type)) && (!n->gate || rows16(n->ldgate, n->type));
-    for (const void *q : ptrs) {
-        if (!on(q, size)) return W4_ERR_ALIGN;
-        vec = vec && on(q, 16);
-    }
-    norm::Args a = {};
-    if (n->quant_fmt) {
-        const w4_status s = check_quantised(n->M, n->D, n->quant_fmt, n->scale_rule, n->global_scale, n->codes,
-                                            n->scales, n->d_status);
-        if (s != W4_OK) return s;
-        if (n->z) return W4_ERR_ARG;
-        a.q = quantised_out(n->D, n->quant_fmt, n->scale_rule, n->global_scale, n->codes, n->scales, n->d_status);
-    } else {
-        if (!n->z || n->ldz < n->D) return W4_ERR_ARG;
-        vec = vec && rows16(n->ldz, n->type);
-    }
-    a.y = n->y, a.h = n->h, a.w_post = n->w_post, a.w_pre = n->w_pre, a.gate = n->gate;
-    a.h_out = n->h_out, a.z = n->z;
-    a.ldy = n->ldy, a.ldh = n->ldh, a.ldgate = n->ldgate, a.ldh_out = n->ldh_out, a.ldz = n->ldz;
-    a.D = n->D, a.gate_rows = n->gate_rows, a.gate_act = n->gate_act;
-    a.residual_scale = n->residual_scale, a.block_scale = n->block_scale, a.eps = n->eps, a.offset = n->weight_offset;
-    cudaStream_t st = as_stream(stream);
-    if (n->quant_fmt && clear_status(n->d_status, st) != W4_OK) return W4_ERR_CUDA;
-    const int mode = vec ? norm::VECTOR : n->quant_fmt ? norm::SCALAR : norm::STRIDED;
-    switch (n->type) {
-    case W4_TYPE_BF16: return launch_norm_fmt<__nv_bfloat16>(a, mode, n->M, n->quant_fmt, st);
-    case W4_TYPE_F16: return launch_norm_fmt<__half>(a, mode, n->M, n->quant_fmt, st);
-    case W4_TYPE_F32: return launch_norm_fmt<float>(a, mode, n->M, n->quant_fmt, st);
-    }
-    return W4_ERR_ARG;
 }
 
 }  // extern "C"
