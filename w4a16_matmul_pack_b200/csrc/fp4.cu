@@ -3,8 +3,6 @@
 // quantise activations to 4 bits and multiply two 4-bit operands.
 #include <cuda_runtime.h>
 
-#include <stdlib.h>
-
 #include <algorithm>
 
 #include "fp4_host.cuh"
@@ -107,49 +105,50 @@ bool codes_map(CUtensorMap &map, const uint8_t *codes, int rows, int K, int box_
 }
 
 template <int FMT, int NT>
-w4_status launch_skinny(const w4_fp4 *a, const w4_fp4 *b, void *y, long long ldy, int out_type, bool early_w,
-                      cudaStream_t st) {
+w4_status launch_skinny(const w4_fp4 *w, const w4_fp4 *x, void *y, long long ldy, int out_type, int splits,
+                        bool early_w, cudaStream_t st) {
     using namespace fgemm;
-    using namespace fgemm::skinny;
-    CUtensorMap amap, bmap;
-    if (!codes_map(amap, a->codes, a->rows, a->K, BM) || !codes_map(bmap, b->codes, b->rows, b->K, NT))
+    CUtensorMap wmap, xmap;
+    if (!codes_map(wmap, w->codes, w->rows, w->K, BM) || !codes_map(xmap, x->codes, x->rows, x->K, NT))
         return W4_ERR_CUDA;
-    int sms = 0;
-    if (device_sms(sms) != W4_OK) return W4_ERR_CUDA;
-    constexpr size_t smem = sizeof(Shared<FMT, NT>) + 1024;
+    constexpr size_t smem = sizeof(skinny::Shared<FMT, NT>) + 1024;
     static_assert(smem <= 227 * 1024, "shared memory of the product");
     auto kernel = skinny::gemm_kernel<FMT, NT>;
     if (!set_smem_limit(reinterpret_cast<const void *>(kernel), smem)) return W4_ERR_CUDA;
-    Params p;
-    p.sfa = a->scales;
-    p.sfb = b->scales;
-    p.ga = FMT == W4_FMT_NVFP4 ? a->global_scale : nullptr;
-    p.gb = FMT == W4_FMT_NVFP4 ? b->global_scale : nullptr;
+    skinny::Params p;
+    p.sfw = w->scales;
+    p.sfx = x->scales;
+    p.gw = FMT == W4_FMT_NVFP4 ? w->global_scale : nullptr;
+    p.gx = FMT == W4_FMT_NVFP4 ? x->global_scale : nullptr;
     p.y = y;
     p.ldy = ldy;
-    p.rows_a = a->rows;
-    p.rows_b = b->rows;
-    p.K = a->K;
-    p.tiles_a = (a->rows + BM - 1) / BM;
-    p.tiles_b = (b->rows + NT - 1) / NT;
-    p.tiles_k = fp4::scale_tiles_k(FMT, a->K);
+    p.N = w->rows;
+    p.M = x->rows;
+    p.K = x->K;
+    p.tiles_n = (w->rows + BM - 1) / BM;
+    p.tiles_k = fp4::scale_tiles_k(FMT, x->K);
+    p.splits = splits;
     p.out_type = out_type;
     p.early_w = early_w;
-    const long long ntiles = (long long)p.tiles_a * p.tiles_b;
-    if (ntiles > kMaxBlocks) return W4_ERR_UNSUPPORTED;
+    const long long blocks = (long long)p.tiles_n * ((x->rows + NT - 1) / NT) * splits;
+    if (blocks > kMaxBlocks) return W4_ERR_UNSUPPORTED;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)std::min<long long>(ntiles, sms), 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.gridDim = dim3((unsigned)blocks, 1, 1);
+    cfg.blockDim = dim3(skinny::kThreads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    // The kernel waits for the previous one on the stream before it reads or
-    // writes global memory; only its prologue overlaps that kernel's tail.
-    cudaLaunchAttribute attr[1];
+    // The kernel waits for the previous one on the stream before it reads x or writes
+    // y (and, without early_w, before it reads w).
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = splits;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, kernel, amap, bmap, p) != cudaSuccess) return W4_ERR_CUDA;
+    cfg.numAttrs = 2;
+    if (cudaLaunchKernelEx(&cfg, kernel, wmap, xmap, p) != cudaSuccess) return W4_ERR_CUDA;
     return launch_status();
 }
 
@@ -182,7 +181,8 @@ bool output_map(CUtensorMap &map, void *y, int rows, int cols, long long ldy, in
 }
 
 template <int FMT, int NT>
-w4_status launch_pair(const w4_fp4 *w, const w4_fp4 *x, void *y, long long ldy, int out_type, cudaStream_t st) {
+w4_status launch_pair(const w4_fp4 *w, const w4_fp4 *x, void *y, long long ldy, int out_type, bool early_w, int sms,
+                      cudaStream_t st) {
     using namespace fgemm;
     using namespace fgemm::pair;
     CUtensorMap xmap, wmap, sxmap, swmap;
@@ -191,8 +191,6 @@ w4_status launch_pair(const w4_fp4 *w, const w4_fp4 *x, void *y, long long ldy, 
         !scales_map(sxmap, x->scales, fp4_scale_bytes(FMT, x->rows, x->K), ST) ||
         !scales_map(swmap, w->scales, fp4_scale_bytes(FMT, w->rows, w->K), ST))
         return W4_ERR_CUDA;
-    int sms = 0;
-    if (device_sms(sms) != W4_OK) return W4_ERR_CUDA;
     constexpr size_t smem = sizeof(pair::Shared<FMT, NT>) + 1024;
     static_assert(smem <= 227 * 1024, "shared memory of the product");
     auto kernel = pair::gemm_kernel<FMT, NT>;
@@ -210,6 +208,7 @@ w4_status launch_pair(const w4_fp4 *w, const w4_fp4 *x, void *y, long long ldy, 
     CUtensorMap ymap = xmap;   // not read without p.out.tma
     if (p.out.tma && !output_map(ymap, y, x->rows, w->rows, ldy, out_type)) return W4_ERR_CUDA;
     p.K = x->K;
+    p.early_w = early_w;
     p.tiles_m = (x->rows + 2 * BM - 1) / (2 * BM);
     p.tiles_n = (w->rows + NT - 1) / NT;
     p.tiles_k = fp4::scale_tiles_k(FMT, x->K);
@@ -233,18 +232,68 @@ w4_status launch_pair(const w4_fp4 *w, const w4_fp4 *x, void *y, long long ldy, 
     return launch_status();
 }
 
+// Slices of K (CTAs of a cluster) for a product of `tiles` tiles of nt tokens: as few
+// stages in a row as possible, an exchange of partial sums counted as the stages that
+// take as long (0.3 us each; measured: 0.6 us at 16 tokens, 3.7 us at 128), and no more
+// CTAs than run at once (at 16 tokens two fit an SM, and a few more than SMs still
+// gain: 9728 x 2560, 9 tokens: 160 CTAs 6.3 us, 80 CTAs 6.7 us; at 64 tokens
+// 152 CTAs 16 us, 76 CTAs 7.2 us).
+int slices(long long tiles, int stages, int nt, int sms) {
+    const long long room = nt <= 16 ? sms + sms / 8 : sms;
+    const int exchange = nt <= 16 ? 2 : nt / 8;
+    int best = 1, cost = stages;
+    for (int s = 2; s <= fgemm::skinny::kMaxSplit && s <= stages && tiles * s <= room; s *= 2) {
+        const int c = (stages + s - 1) / s + exchange;
+        if (c < cost) best = s, cost = c;
+    }
+    return best;
+}
+
+template <int FMT, int NT>
+w4_status few_tokens(const w4_fp4 *w, const w4_fp4 *x, void *y, long long ldy, int out_type, bool early_w, int sms,
+                     cudaStream_t st) {
+    const long long tiles = (w->rows + fgemm::BM - 1) / fgemm::BM;
+    const int s = slices(tiles, (w->K + fgemm::BK - 1) / fgemm::BK, NT, sms);
+    return launch_skinny<FMT, NT>(w, x, y, ldy, out_type, s, early_w, st);
+}
+
+// Width of a prompt's tiles: the least of launch + waves x (stages x time per stage +
+// time per tile), in us as measured on 148 SMs.  A stage is bound by its loads (0.31
+// us for 256 tokens x 256 rows, 0.255 for 192, 0.24 for 128); tiles of 256 rows share
+// tensor memory between two accumulators and wait for it (1.8 us a tile).  2048 x 2560 x
+// 9728: 23.6 us at 192, 27.5 at 256, 29.6 at 128; 8192 x 9728 x 2560: 73.9 at 256, 77.8
+// at 192.
+int tile_width(int M, int N, int K, int sms) {
+    const struct { int nt; double launch, stage, tile; } kinds[] = {
+        {128, 5.2, 0.24, 0.3}, {192, 5.6, 0.255, 0.4}, {256, 5.9, 0.31, 1.8}};
+    const long long pairs = std::max(1, sms / 2), stages = (K + fgemm::BK - 1) / fgemm::BK;
+    int best = 0;
+    double least = 0;
+    for (const auto &k : kinds) {
+        const long long tiles = (long long)((M + 255) / 256) * ((N + k.nt - 1) / k.nt);
+        const double t = k.launch + (double)((tiles + pairs - 1) / pairs) * (stages * k.stage + k.tile);
+        if (!best || t < least) best = k.nt, least = t;
+    }
+    return best;
+}
+
 template <int FMT>
 w4_status gemm_fmt(const w4_fp4 *w, const w4_fp4 *x, void *y, long long ldy, int out_type, bool early_w,
                    cudaStream_t st) {
     const int M = x->rows;
-    if (M <= 16) return launch_skinny<FMT, 16>(w, x, y, ldy, out_type, early_w, st);
-    if (M <= 64) return launch_skinny<FMT, 64>(w, x, y, ldy, out_type, early_w, st);
-    if (M <= 128) return launch_skinny<FMT, 128>(w, x, y, ldy, out_type, early_w, st);
-    const char *e = getenv("W4_NT");
-    const int nt = e ? atoi(e) : 256;
-    if (nt == 192) return launch_pair<FMT, 192>(w, x, y, ldy, out_type, st);
-    if (nt == 128) return launch_pair<FMT, 128>(w, x, y, ldy, out_type, st);
-    return launch_pair<FMT, 256>(w, x, y, ldy, out_type, st);
+    int sms = 0;
+    if (device_sms(sms) != W4_OK) return W4_ERR_CUDA;
+    // up to 128 tokens fit one tile of the kernel that streams weights (128 tokens,
+    // 2560 x 2560: 7.9 us; a pair's tile of 256 tokens would be half empty)
+    if (M <= 16) return few_tokens<FMT, 16>(w, x, y, ldy, out_type, early_w, sms, st);
+    if (M <= 32) return few_tokens<FMT, 32>(w, x, y, ldy, out_type, early_w, sms, st);
+    if (M <= 64) return few_tokens<FMT, 64>(w, x, y, ldy, out_type, early_w, sms, st);
+    if (M <= 128) return few_tokens<FMT, 128>(w, x, y, ldy, out_type, early_w, sms, st);
+    switch (tile_width(M, w->rows, w->K, sms)) {
+    case 128: return launch_pair<FMT, 128>(w, x, y, ldy, out_type, early_w, sms, st);
+    case 192: return launch_pair<FMT, 192>(w, x, y, ldy, out_type, early_w, sms, st);
+    default: return launch_pair<FMT, 256>(w, x, y, ldy, out_type, early_w, sms, st);
+    }
 }
 
 w4_status check_product(const w4_fp4 *w, const w4_fp4 *x, const void *y, long long ldy, int out_type) {

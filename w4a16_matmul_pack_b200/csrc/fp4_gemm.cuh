@@ -77,6 +77,7 @@ struct Params {
     Output out;
     int K;
     int tiles_m, tiles_n, tiles_k; // tiles_k: scale tiles along K
+    int early_w;                   // the weights may be read before the previous kernel has completed
 };
 
 // Arrives on the barrier at this offset in both CTAs once the MMAs and copies
@@ -156,33 +157,46 @@ __global__ void __launch_bounds__(kThreads, 1)
     cluster_sync();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, sh.tmem_base, 0);
-    // x may be the previous kernel's output (programmatic dependent launch)
-    pdl_wait_prior_grid();
-
     if (warp == 0) {
         // ------------------------------ TMA producer ------------------------------
-        int it = 0;
+        // scale tiles are loaded as rows of 128 words; those past a row's last (read from the
+        // next group, or zeros past the end) are not used
+        auto load_w = [&](int t, int kt, int s) {
+            const int tn = t / p.tiles_m;
+            if (rank == 0) mbar_arrive_expect_tx(&sh.full[s], 2 * C::STAGE_BYTES);
+            const uint32_t full = in_first_cta(&sh.full[s]);
+            tma_load_pair(sh.b[s], &wmap, kt * (BK / 2), tn * NT + (int)rank * (NT / 2), full);
+#pragma unroll
+            for (int g = 0; g < C::GB; g++)
+                tma_load_pair(sh.sfb[s][g], &swmap, 0, (tn * NT / 128 + g) * p.tiles_k + kt * C::ST, full);
+        };
+        auto load_x = [&](int t, int kt, int s) {
+            const int m0 = (t % p.tiles_m) * 2 * BM + (int)rank * BM;
+            const uint32_t full = in_first_cta(&sh.full[s]);
+            tma_load_pair(sh.a[s], &xmap, kt * (BK / 2), m0, full);
+            tma_load_pair(sh.sfa[s], &sxmap, 0, (m0 / 128) * p.tiles_k + kt * C::ST, full);
+        };
+        // The first tile's first stages: their weights may be on the way while the previous
+        // kernel (which makes x) still runs.
+        const int first = pair0 < ntiles ? min(KT, STAGES) : 0;
+        if (!p.early_w) pdl_wait_prior_grid();
+        for (int i = 0; i < first; i++)
+            if (elect_one()) load_w(pair0, i, i);
+        if (p.early_w) pdl_wait_prior_grid();
+        for (int i = 0; i < first; i++)
+            if (elect_one()) load_x(pair0, i, i);
+        int it = first;
         bool stop = false;
         for (int t = pair0; t < ntiles && !stop; t += pairs) {
-            const int tm = t % p.tiles_m, tn = t / p.tiles_m;
-            const int m0 = tm * 2 * BM + (int)rank * BM, n0 = tn * NT + (int)rank * (NT / 2);
-            for (int kt = 0; kt < KT; kt++, it++) {
+            for (int kt = t == pair0 ? first : 0; kt < KT; kt++, it++) {
                 const int s = it % STAGES;
                 if (it >= STAGES) pipe_wait(&sh.empty[s], ((it / STAGES) - 1) & 1, abort, limit);
                 // after an abort nothing more is loaded: the stage may not be free
                 stop = __any_sync(0xFFFFFFFFu, *abort != 0);
                 if (stop) break;
                 if (elect_one()) {
-                    if (rank == 0) mbar_arrive_expect_tx(&sh.full[s], 2 * C::STAGE_BYTES);
-                    const uint32_t full = in_first_cta(&sh.full[s]);
-                    tma_load_pair(sh.a[s], &xmap, kt * (BK / 2), m0, full);
-                    tma_load_pair(sh.b[s], &wmap, kt * (BK / 2), n0, full);
-                    // scale tiles as rows of 128 words; those past a row's last (read from
-                    // the next group, or zeros past the end) are not used
-                    tma_load_pair(sh.sfa[s], &sxmap, 0, (m0 / 128) * p.tiles_k + kt * C::ST, full);
-#pragma unroll
-                    for (int g = 0; g < C::GB; g++)
-                        tma_load_pair(sh.sfb[s][g], &swmap, 0, (tn * NT / 128 + g) * p.tiles_k + kt * C::ST, full);
+                    load_w(t, kt, s);
+                    load_x(t, kt, s);
                 }
             }
         }
@@ -249,6 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         // -------------------------------- epilogue --------------------------------
         const int q = warp & 3, half = (warp - kEpiWarp0) >> 2;
+        pdl_wait_prior_grid();   // y and the global scales belong to the previous kernel until then
         const Factor fac(p.gx, p.gw);
         int lt = 0;
         for (int t = pair0; t < ntiles; t += pairs, lt++) {

@@ -171,11 +171,8 @@ __device__ __forceinline__ void tmem_ld64(uint32_t taddr, float (&v)[64]) {
 template <int n>
 __device__ __forceinline__ void apply_factor(const Factor &f, float (&v)[n]) {
     if (f.wide) {
-#pragma unroll 1
-        for (int i = 0; i < n; i += 8)
 #pragma unroll
-            for (int j = 0; j < n; j++)
-                if (j >= i && j < i + 8) v[j] = (float)((double)v[j] * f.d);
+        for (int i = 0; i < n; i++) v[i] = (float)((double)v[i] * f.d);
     } else {
 #pragma unroll
         for (int i = 0; i < n; i++) v[i] *= f.f;
@@ -256,9 +253,9 @@ __device__ __forceinline__ void store_rows(const Output &o, const CUtensorMap *m
     }
 }
 
-// Before the warp's staging buffer goes out of use: its boxes have been written.
+// Before the warp's staging buffer goes out of use: its boxes have been read.
 __device__ __forceinline__ void store_rows_done() {
-    if (elect_one()) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    if (elect_one()) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
     __syncwarp();
 }
 

@@ -1,14 +1,20 @@
-// fp4_skinny.cuh -- W4A4 product with one CTA per tile (sm_100a): few tokens.
-// (see fp4_mma.cuh for the instructions both product kernels use)
+// fp4_skinny.cuh -- W4A4 product for few tokens and for small outputs (sm_100a),
+// one CTA per tile and slice of K (fp4_gemm.cuh: the instructions and the formula).
 //
 // Tile: 128 rows of w (the operand A, tensor-memory lanes) x NT tokens (B) x 256 k
 // per stage: no work is wasted on missing tokens, and the lanes of an epilogue
-// store run along a row of y.
+// store run along a row of y.  Such a product streams weights: what counts is how
+// many SMs load at once and how soon the first byte arrives.
+//   - A few tiles do not fill the GPU, so the K of a tile is shared out to the S CTAs
+//     of a cluster.  Each sends the partial sums of NT / S tokens to each of the others
+//     through distributed shared memory and adds those of its own tokens in the order
+//     of the slices (deterministic, no workspace).
+//   - With W4_LAUNCH_PDL the first stages' weights are on their way while the previous
+//     kernel (the quantiser or the norm that makes x) still runs.
 //
-// Warp roles (6 warps): 0 TMA producer; 1 tensor-memory allocation, scale copies
-// and MMAs (one lane); 2-5 epilogue (warp w reads lanes 32 (w % 4) .. + 31).
-// Persistent CTAs, one per SM; two accumulators, so the epilogue of a tile
-// overlaps the next tile's MMAs.  Every mbarrier wait is bounded (common.cuh).
+// Warp roles (6 warps): 0 TMA producer; 1 tensor-memory allocation, scale copies and
+// MMAs; 2-5 epilogue (warp w reads lanes 32 (w % 4) .. + 31).  Every mbarrier wait is
+// bounded (fp4_mma.cuh).
 #pragma once
 
 #include "fp4_mma.cuh"
@@ -19,59 +25,109 @@ namespace fgemm {
 
 namespace skinny {
 
-constexpr int STAGES = 4;
 constexpr int kWarps = 6;
 constexpr int kThreads = kWarps * 32;
-constexpr int kEpiWarps = 4;
+constexpr int kEpiWarp0 = 2;
+constexpr int kMaxSplit = 8;
 
 template <int FMT, int NT>
 struct Config {
     static constexpr int ST = Scales<FMT>::TILES;
-    static constexpr int GB = (NT + 127) / 128;                 // 128-row groups of a B tile
     static constexpr uint32_t B_BYTES = NT * (BK / 2);
-    static constexpr uint32_t SF_COLS = 4 * ST * (1 + GB);      // tensor-memory columns of a stage's scales
+    static constexpr uint32_t STAGE_BYTES = A_BYTES + B_BYTES + 2 * ST * SF_TILE;
+    static constexpr uint32_t RED_BYTES = NT * BM * 4;                      // partial sums of NT / S tokens x S slices
+    // two CTAs per SM where the partial sums are small
+    static constexpr uint32_t BUDGET = NT <= 32 ? 112 * 1024 : 224 * 1024;
+    static constexpr int STAGES = (int)((BUDGET - RED_BYTES - 2048) / STAGE_BYTES) < 8
+                                      ? (int)((BUDGET - RED_BYTES - 2048) / STAGE_BYTES) : 8;
+    static constexpr uint32_t SF_COLS = 4 * ST * 2;                         // scales of w and of x, one stage
     static constexpr uint32_t ACC_COLS = NT < 32 ? 32 : NT;
-    static constexpr uint32_t SF_COL0 = 2 * ACC_COLS;
-    static constexpr uint32_t TMEM_COLS = pow2_at_least(SF_COL0 + SF_COLS);
-    static_assert(TMEM_COLS <= 512, "tensor memory");
+    static constexpr uint32_t TMEM_COLS = pow2_at_least(ACC_COLS + SF_COLS);
+    static_assert(NT % 16 == 0 && NT <= 128 && STAGES >= 3 && TMEM_COLS <= 512, "tile");
 };
 
 template <int FMT, int NT>
 struct Shared {
     using C = Config<FMT, NT>;
-    uint8_t a[STAGES][A_BYTES];                              // 1024-byte aligned (swizzle atoms)
-    uint8_t b[STAGES][C::B_BYTES];
-    uint8_t sfa[STAGES][C::ST][SF_TILE];
-    uint8_t sfb[STAGES][C::GB][C::ST][SF_TILE];
-    uint64_t full[STAGES], empty[STAGES];
-    uint64_t acc_full[2], acc_empty[2];
-    uint64_t mma_done;
+    uint8_t a[C::STAGES][A_BYTES];                 // 1024-byte aligned (swizzle atoms)
+    uint8_t b[C::STAGES][C::B_BYTES];
+    uint8_t sfa[C::STAGES][C::ST][SF_TILE];
+    uint8_t sfb[C::STAGES][C::ST][SF_TILE];
+    float red[NT * BM];                            // [slice][token of this CTA][row of w]
+    uint64_t full[C::STAGES], empty[C::STAGES];
+    uint64_t acc_full, mma_done;
     uint32_t tmem_base;
     int abort;
 };
 
 struct Params {
-    const uint8_t *sfa, *sfb;      // scale tiles of A and B
-    const float *ga, *gb;          // global scales (NVFP4) or null
+    const uint8_t *sfw, *sfx;      // scale tiles
+    const float *gw, *gx;          // global scales (NVFP4) or null
     void *y;
     long long ldy;
-    int rows_a, rows_b, K;
-    int tiles_a, tiles_b, tiles_k; // tiles_k: scale tiles along K
+    int N, M, K;
+    int tiles_n, tiles_k;          // tiles_k: scale tiles along K
+    int splits;                    // CTAs of a cluster: slices of K
     int out_type;
     int early_w;                   // the weights may be read before the previous kernel has completed
 };
 
+// The first `count` of n values of consecutive tokens, one column of y per lane.
+template <int n>
+__device__ __forceinline__ void store_column(const Params &p, int m, int col, int count, const float (&v)[n]) {
+    const size_t at = (size_t)m * p.ldy + col;
+    if (p.out_type == OUT_F32) {
+        float *o = reinterpret_cast<float *>(p.y) + at;
+#pragma unroll
+        for (int j = 0; j < n; j++, o += p.ldy)
+            if (j < count) *o = v[j];
+    } else {
+        uint16_t *o = reinterpret_cast<uint16_t *>(p.y) + at;
+#pragma unroll
+        for (int j = 0; j < n; j += 2) {
+            const uint32_t w = pack16(v[j], v[j + 1 < n ? j + 1 : j], p.out_type);
+            if (j < count) *o = (uint16_t)w;
+            o += p.ldy;
+            if (j + 1 < count) *o = (uint16_t)(w >> 16);
+            o += p.ldy;
+        }
+    }
+}
+
+// Tokens first .. first + own - 1 of column n0 + row: the slices' partial sums in order.
+template <int n>
+__device__ __forceinline__ void add_slices(const Params &p, const Factor &fac, const float *red, int own, int first,
+                                           int n0, int row) {
+#pragma unroll 1
+    for (int i = 0; i < own && first + i < p.M; i += n) {
+        float v[n];
+#pragma unroll
+        for (int j = 0; j < n; j++) v[j] = red[(i + j) * BM + row];
+#pragma unroll 1
+        for (int k = 1; k < p.splits; k++)
+#pragma unroll
+            for (int j = 0; j < n; j++) v[j] += red[(k * own + i + j) * BM + row];
+        apply_factor(fac, v);
+        store_column(p, first + i, n0 + row, p.M - first - i, v);
+    }
+}
+
 template <int FMT, int NT>
-__global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant__ CUtensorMap amap,
-                                                            const __grid_constant__ CUtensorMap bmap,
-                                                            const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kThreads, 2) gemm_kernel(const __grid_constant__ CUtensorMap wmap,
+                                                         const __grid_constant__ CUtensorMap xmap,
+                                                         const __grid_constant__ Params p) {
     using S = Shared<FMT, NT>;
     using C = Config<FMT, NT>;
+    constexpr int STAGES = C::STAGES;
     extern __shared__ uint8_t smem_raw[];
     S &sh = *reinterpret_cast<S *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const int tile = blockIdx.x / p.splits, slice = blockIdx.x % p.splits;
+    const int n0 = (tile % p.tiles_n) * BM, m0 = (tile / p.tiles_n) * NT;
+    // stages of this slice: the first KT % splits slices take one more
     const int KT = (p.K + BK - 1) / BK;
-    const int ntiles = p.tiles_a * p.tiles_b;
+    const int k0 = slice * (KT / p.splits) + min(slice, KT % p.splits);
+    const int k1 = k0 + KT / p.splits + (slice < KT % p.splits ? 1 : 0);
     volatile int *abort = &sh.abort;
     const unsigned long long limit = g_wait_limit_ns;
 
@@ -81,10 +137,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             mbar_init(&sh.full[i], 1);
             mbar_init(&sh.empty[i], 1);
         }
-        for (int i = 0; i < 2; i++) {
-            mbar_init(&sh.acc_full[i], 1);
-            mbar_init(&sh.acc_empty[i], kEpiWarps);
-        }
+        mbar_init(&sh.acc_full, 1);
         mbar_init(&sh.mma_done, 1);
         fence_mbar_init();
     }
@@ -95,81 +148,77 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
     }
     tc_fence_before();
     __syncthreads();
+    // (first half of a cluster barrier: a CTA's shared memory is written by others once
+    // it is known to run)
+    if (p.splits > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, sh.tmem_base, 0);
-    // x may be the previous kernel's output (programmatic dependent launch)
-    pdl_wait_prior_grid();
 
     if (warp == 0) {
         // ------------------------------ TMA producer ------------------------------
-        int it = 0;
-        bool stop = false;
-        for (int t = blockIdx.x; t < ntiles && !stop; t += gridDim.x) {
-            const int ta = t % p.tiles_a, tb = t / p.tiles_a;
-            const int groups_b = min(C::GB, (p.rows_b + 127) / 128 - tb * NT / 128);
-            for (int kt = 0; kt < KT; kt++, it++) {
-                const int s = it % STAGES;
-                if (it >= STAGES) pipe_wait(&sh.empty[s], ((it / STAGES) - 1) & 1, abort, limit);
-                // after an abort nothing more is loaded: the stage may not be free
-                stop = __any_sync(0xFFFFFFFFu, *abort != 0);
-                if (stop) break;
-                // scale tiles that exist in this stage (the last one of a row may be cut)
-                const int nt = min(C::ST, p.tiles_k - kt * C::ST);
-                if (elect_one()) {
-                    mbar_arrive_expect_tx(&sh.full[s],
-                                          A_BYTES + C::B_BYTES + (uint32_t)(nt * (1 + groups_b)) * SF_TILE);
-                    tma_load_2d(sh.a[s], &amap, kt * (BK / 2), ta * BM, &sh.full[s]);
-                    tma_load_2d(sh.b[s], &bmap, kt * (BK / 2), tb * NT, &sh.full[s]);
-                    bulk_load(sh.sfa[s], p.sfa + ((size_t)ta * p.tiles_k + kt * C::ST) * SF_TILE,
-                              (uint32_t)nt * SF_TILE, &sh.full[s]);
-                    for (int g = 0; g < groups_b; g++)
-                        bulk_load(sh.sfb[s][g],
-                                  p.sfb + ((size_t)(tb * NT / 128 + g) * p.tiles_k + kt * C::ST) * SF_TILE,
-                                  (uint32_t)nt * SF_TILE, &sh.full[s]);
-                }
+        // scale tiles that exist in a stage (the last stage of a row may be cut)
+        auto tiles = [&](int kt) { return min(C::ST, p.tiles_k - kt * C::ST); };
+        auto load_w = [&](int kt, int s) {
+            mbar_arrive_expect_tx(&sh.full[s], A_BYTES + C::B_BYTES + 2 * (uint32_t)tiles(kt) * SF_TILE);
+            tma_load_2d(sh.a[s], &wmap, kt * (BK / 2), n0, &sh.full[s]);
+            bulk_load(sh.sfa[s], p.sfw + ((size_t)(n0 / 128) * p.tiles_k + kt * C::ST) * SF_TILE,
+                      (uint32_t)tiles(kt) * SF_TILE, &sh.full[s]);
+        };
+        auto load_x = [&](int kt, int s) {
+            tma_load_2d(sh.b[s], &xmap, kt * (BK / 2), m0, &sh.full[s]);
+            bulk_load(sh.sfb[s], p.sfx + ((size_t)(m0 / 128) * p.tiles_k + kt * C::ST) * SF_TILE,
+                      (uint32_t)tiles(kt) * SF_TILE, &sh.full[s]);
+        };
+        const int first = min(k1 - k0, STAGES);
+        if (!p.early_w) pdl_wait_prior_grid();
+        for (int i = 0; i < first; i++)
+            if (elect_one()) load_w(k0 + i, i);
+        if (p.early_w) pdl_wait_prior_grid();   // x may be the previous kernel's output
+        for (int i = 0; i < first; i++)
+            if (elect_one()) load_x(k0 + i, i);
+        int it = first;
+        for (; it < k1 - k0; it++) {
+            const int s = it % STAGES;
+            pipe_wait(&sh.empty[s], ((it / STAGES) - 1) & 1, abort, limit);
+            // after an abort nothing more is loaded: the stage may not be free
+            if (__any_sync(0xFFFFFFFFu, *abort != 0)) break;
+            if (elect_one()) {
+                load_w(k0 + it, s);
+                load_x(k0 + it, s);
             }
         }
         drain_ring(sh.full, STAGES, it);
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------- MMA issuer -------------------------------
-        int it = 0, lt = 0;
-        bool stop = false;
         const int steps = (p.K + 63) / 64;
-        for (int t = blockIdx.x; t < ntiles && !stop; t += gridDim.x, lt++) {
-            const uint32_t acc = tmem + (uint32_t)(lt & 1) * C::ACC_COLS;
-            if (lt >= 2) pipe_wait(&sh.acc_empty[lt & 1], ((lt >> 1) - 1) & 1, abort, limit);
-            for (int kt = 0; kt < KT; kt++, it++) {
-                const int s = it % STAGES;
-                pipe_wait(&sh.full[s], (it / STAGES) & 1, abort, limit);
-                stop = __any_sync(0xFFFFFFFFu, *abort != 0);
-                if (stop) break;
-                tc_fence_after();
-                if (elect_one()) {
-                    const uint32_t sfa = tmem + C::SF_COL0, sfb = sfa + 4 * C::ST;
-                    const uint32_t a = codes_desc(smem_addr(sh.a[s])), b = codes_desc(smem_addr(sh.b[s]));
-                    const uint32_t fa = scale_desc(smem_addr(sh.sfa[s])), fb = scale_desc(smem_addr(sh.sfb[s]));
+        const uint32_t sfa = tmem + C::ACC_COLS, sfb = sfa + 4 * C::ST;
+        for (int it = 0; it < k1 - k0; it++) {
+            const int s = it % STAGES, kt = k0 + it;
+            pipe_wait(&sh.full[s], (it / STAGES) & 1, abort, limit);
+            if (__any_sync(0xFFFFFFFFu, *abort != 0)) break;
+            tc_fence_after();
+            if (elect_one()) {
+                const uint32_t a = codes_desc(smem_addr(sh.a[s])), b = codes_desc(smem_addr(sh.b[s]));
+                const uint32_t fa = scale_desc(smem_addr(sh.sfa[s])), fb = scale_desc(smem_addr(sh.sfb[s]));
 #pragma unroll
-                    for (int c = 0; c < C::ST; c++) {
-                        if (kt * C::ST + c < p.tiles_k) {
-                            copy_scales<1>(sfa + 4 * c, fa + c * (SF_TILE / 16));
-#pragma unroll
-                            for (int g = 0; g < C::GB; g++)
-                                copy_scales<1>(sfb + 4 * (c * C::GB + g), fb + (g * C::ST + c) * (SF_TILE / 16));
-                        }
+                for (int c = 0; c < C::ST; c++) {
+                    if (kt * C::ST + c < p.tiles_k) {
+                        copy_scales<1>(sfa + 4 * c, fa + c * (SF_TILE / 16));
+                        copy_scales<1>(sfb + 4 * c, fb + c * (SF_TILE / 16));
                     }
-#pragma unroll
-                    for (int j = 0; j < BK / 64; j++) {
-                        const int c = j / Scales<FMT>::STEPS_PER_TILE;
-                        if (kt * (BK / 64) + j < steps)
-                            mma_fp4<FMT, 1>(acc, a + 2 * j, b + 2 * j, idesc<FMT>(BM, NT) | scale_ids<FMT>(j),
-                                            sfa + 4 * c, sfb + 4 * c * C::GB, (kt | j) ? 1u : 0u);
-                    }
-                    mma_commit(&sh.empty[s]);
-                    if (kt == KT - 1) mma_commit(&sh.acc_full[lt & 1]);
                 }
-                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < BK / 64; j++) {
+                    const int c = j / Scales<FMT>::STEPS_PER_TILE;
+                    if (kt * (BK / 64) + j < steps)
+                        mma_fp4<FMT, 1>(tmem, a + 2 * j, b + 2 * j, idesc<FMT>(BM, NT) | scale_ids<FMT>(j),
+                                        sfa + 4 * c, sfb + 4 * c, (it | j) ? 1u : 0u);
+                }
+                mma_commit(&sh.empty[s]);
+                if (it == k1 - k0 - 1) mma_commit(&sh.acc_full);
             }
+            __syncwarp();
         }
         // tensor memory is released after the final barrier: every MMA and copy
         // issued must have completed by then (also after an abort)
@@ -177,41 +226,52 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
         __syncwarp();
         mbar_wait_bounded(&sh.mma_done, 0);
         __syncwarp();
-    } else {
-        // -------------------------------- epilogue --------------------------------
-        const int q = warp & 3;
-        const Factor fac(p.ga, p.gb);
-        int lt = 0;
-        for (int t = blockIdx.x; t < ntiles; t += gridDim.x, lt++) {
-            const int b = lt & 1;
-            const int n = (t % p.tiles_a) * BM + q * 32 + lane;    // this lane's row of w
-            // on expiry (abort) the accumulator is garbage, but the warp stays together
-            pipe_wait(&sh.acc_full[b], (lt >> 1) & 1, abort, limit);
-            __syncwarp();
-            tc_fence_after();
-            for (int c = 0; c < NT / 16; c++) {
-                uint32_t r[16];
-                W4_FP4_TMEM_LD16(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * C::ACC_COLS + c * 16), r);
-                asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+    }
+
+    // -------------------------------- epilogue --------------------------------
+    const int q = warp & 3, row = q * 32 + lane;            // row of w in the tile
+    const int own = NT / p.splits;                          // tokens a CTA of the cluster adds up (a power of two)
+    if (p.splits > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (warp >= kEpiWarp0) {
+        pdl_wait_prior_grid();                              // y and the global scales belong to it until then
+        // on expiry (abort) the accumulator is garbage, but the warp stays together
+        pipe_wait(&sh.acc_full, 0, abort, limit);
+        __syncwarp();
+        tc_fence_after();
+        const Factor fac(p.gw, p.gx);
+        const int n = n0 + row, shift = 31 - __clz(own);
+#pragma unroll 1
+        for (int c = 0; c < NT / 16 && m0 + c * 16 < p.M; c++) {
+            uint32_t r[16];
+            W4_FP4_TMEM_LD16(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(c * 16), r);
+            asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+            if (p.splits > 1) {
+#pragma unroll
+                for (int j = 0; j < 16; j++) {
+                    const int m = c * 16 + j, to = m >> shift;   // the CTA that adds token m
+                    const uint32_t here = smem_addr(sh.red) + 4u * (uint32_t)((slice * own + m - (to << shift)) * BM + row);
+                    uint32_t there;
+                    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(here), "r"(to));
+                    asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(there), "r"(r[j]) : "memory");
+                }
+            } else if (n < p.N) {
                 float v[16];
 #pragma unroll
                 for (int j = 0; j < 16; j++) v[j] = __uint_as_float(r[j]);
                 apply_factor(fac, v);
-                if (n >= p.rows_a) continue;
-                const int m0 = (t / p.tiles_a) * NT + c * 16, count = min(16, p.rows_b - m0);
-#pragma unroll
-                for (int j = 0; j < 16; j++) {
-                    if (j >= count) break;
-                    const size_t i = (size_t)(m0 + j) * p.ldy + n;
-                    if (p.out_type == OUT_F32) reinterpret_cast<float *>(p.y)[i] = v[j];
-                    else reinterpret_cast<uint16_t *>(p.y)[i] = (uint16_t)pack16(v[j], v[j], p.out_type);
-                }
+                store_column(p, m0 + c * 16, n, p.M - m0 - c * 16, v);
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.acc_empty[b]);
         }
-        __syncwarp();
+    }
+    if (p.splits > 1) {
+        // all partial sums are in place; after this no CTA touches another's shared memory
+        asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+        if (warp >= kEpiWarp0 && n0 + row < p.N) {
+            const Factor fac(p.gw, p.gx);
+            const int first = m0 + slice * own;
+            if (own >= 8) add_slices<8>(p, fac, sh.red, own, first, n0, row);
+            else add_slices<2>(p, fac, sh.red, own, first, n0, row);
+        }
     }
 
     tc_fence_before();
