@@ -18,7 +18,7 @@
 // and the scales do not fit, so they share the middle columns: the epilogue
 // drains those first, and the next tile's MMAs start when they are free.
 //
-// Warp roles (10 warps, both CTAs unless said): 0 TMA producer; 1 tensor-memory
+// Warp roles (11 warps, both CTAs unless said): 0 and 10 TMA producers; 1 tensor-memory
 // allocation, scale copies and MMAs (one lane of the first CTA); 2-9 epilogue (warp
 // w reads lanes 32 (w % 4) .. + 31, every second chunk of 32 columns).  Every
 // mbarrier wait is bounded (fp4_mma.cuh).
@@ -34,7 +34,8 @@ namespace pair {
 
 constexpr int kEpiWarps = 8;
 constexpr int kEpiWarp0 = 2;
-constexpr int kWarps = kEpiWarp0 + kEpiWarps;
+constexpr int kXWarp = kEpiWarp0 + kEpiWarps;
+constexpr int kWarps = kXWarp + 1;
 constexpr int kThreads = kWarps * 32;
 constexpr int CHUNK = 64;                // accumulator columns per epilogue step
 constexpr uint32_t kSmemBudget = 225 * 1024 - kEpiWarps * OUT_BYTES;
@@ -157,53 +158,45 @@ __global__ void __launch_bounds__(kThreads, 1)
     cluster_sync();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, sh.tmem_base, 0);
-    if (warp == 0) {
-        // ------------------------------ TMA producer ------------------------------
-        // scale tiles are loaded as rows of 128 words; those past a row's last (read from the
-        // next group, or zeros past the end) are not used
-        auto load_w = [&](int t, int kt, int s) {
-            const int tn = t / p.tiles_m;
-            if (rank == 0) mbar_arrive_expect_tx(&sh.full[s], 2 * C::STAGE_BYTES);
-            const uint32_t full = in_first_cta(&sh.full[s]);
-            tma_load_pair(sh.b[s], &wmap, kt * (BK / 2), tn * NT + (int)rank * (NT / 2), full);
-#pragma unroll
-            for (int g = 0; g < C::GB; g++)
-                tma_load_pair(sh.sfb[s][g], &swmap, 0, (tn * NT / 128 + g) * p.tiles_k + kt * C::ST, full);
-        };
-        auto load_x = [&](int t, int kt, int s) {
-            const int m0 = (t % p.tiles_m) * 2 * BM + (int)rank * BM;
-            const uint32_t full = in_first_cta(&sh.full[s]);
-            tma_load_pair(sh.a[s], &xmap, kt * (BK / 2), m0, full);
-            tma_load_pair(sh.sfa[s], &sxmap, 0, (m0 / 128) * p.tiles_k + kt * C::ST, full);
-        };
-        // The first tile's first stages: their weights may be on the way while the previous
-        // kernel (which makes x) still runs.
-        const int first = pair0 < ntiles ? min(KT, STAGES) : 0;
-        if (!p.early_w) pdl_wait_prior_grid();
-        for (int i = 0; i < first; i++)
-            if (elect_one()) load_w(pair0, i, i);
-        if (p.early_w) pdl_wait_prior_grid();
-        for (int i = 0; i < first; i++)
-            if (elect_one()) load_x(pair0, i, i);
-        int it = first;
+    if (warp == 0 || warp == kXWarp) {
+        // ------------------------------ TMA producers ------------------------------
+        // Warp 0 loads w, warp kXWarp x (one warp for both: 8192 x 9728 x 2560 NVFP4 81.7
+        // us, two 77.6 us).  With early_w the weights of the first stages are on
+        // the way while the previous kernel (which makes x) still runs.
+        const bool is_w = warp == 0;
+        if (!is_w || !p.early_w) pdl_wait_prior_grid();
+        int it = 0;
         bool stop = false;
         for (int t = pair0; t < ntiles && !stop; t += pairs) {
-            for (int kt = t == pair0 ? first : 0; kt < KT; kt++, it++) {
+            const int m0 = (t % p.tiles_m) * 2 * BM + (int)rank * BM, tn = t / p.tiles_m;
+            const int n0 = tn * NT + (int)rank * (NT / 2);
+            for (int kt = 0; kt < KT; kt++, it++) {
                 const int s = it % STAGES;
                 if (it >= STAGES) pipe_wait(&sh.empty[s], ((it / STAGES) - 1) & 1, abort, limit);
                 // after an abort nothing more is loaded: the stage may not be free
                 stop = __any_sync(0xFFFFFFFFu, *abort != 0);
                 if (stop) break;
                 if (elect_one()) {
-                    load_w(t, kt, s);
-                    load_x(t, kt, s);
+                    const uint32_t full = in_first_cta(&sh.full[s]);
+                    // scale tiles are rows of 128 words; those past a row's last (read from the
+                    // next group, or zeros past the end) are not used
+                    if (is_w) {
+                        if (rank == 0) mbar_arrive_expect_tx(&sh.full[s], 2 * C::STAGE_BYTES);
+                        tma_load_pair(sh.b[s], &wmap, kt * (BK / 2), n0, full);
+#pragma unroll
+                        for (int g = 0; g < C::GB; g++)
+                            tma_load_pair(sh.sfb[s][g], &swmap, 0, (tn * NT / 128 + g) * p.tiles_k + kt * C::ST, full);
+                    } else {
+                        tma_load_pair(sh.a[s], &xmap, kt * (BK / 2), m0, full);
+                        tma_load_pair(sh.sfa[s], &sxmap, 0, (m0 / 128) * p.tiles_k + kt * C::ST, full);
+                    }
                 }
             }
         }
         // no load may land and no commit arrive after this CTA has left: the first CTA
         // waits for both CTAs' loads, each for the MMAs' arrivals on its own barriers,
         // and both meet in the cluster barrier at the end
-        if (rank == 0) drain_ring(sh.full, STAGES, it);
+        if (rank == 0 && is_w) drain_ring(sh.full, STAGES, it);
         for (int i = max(0, it - STAGES); i < it; i++)
             pipe_wait(&sh.empty[i % STAGES], (i / STAGES) & 1, abort, limit);
         __syncwarp();

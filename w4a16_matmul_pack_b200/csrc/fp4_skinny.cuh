@@ -169,17 +169,16 @@ __global__ void __launch_bounds__(kThreads, 2) gemm_kernel(const __grid_constant
             bulk_load(sh.sfb[s], p.sfx + ((size_t)(m0 / 128) * p.tiles_k + kt * C::ST) * SF_TILE,
                       (uint32_t)tiles(kt) * SF_TILE, &sh.full[s]);
         };
-        const int first = min(k1 - k0, STAGES);
-        if (!p.early_w) pdl_wait_prior_grid();
+        const int first = p.early_w ? min(k1 - k0, STAGES) : 0;
         for (int i = 0; i < first; i++)
             if (elect_one()) load_w(k0 + i, i);
-        if (p.early_w) pdl_wait_prior_grid();   // x may be the previous kernel's output
+        pdl_wait_prior_grid();   // x may be the previous kernel's output
         for (int i = 0; i < first; i++)
             if (elect_one()) load_x(k0 + i, i);
         int it = first;
         for (; it < k1 - k0; it++) {
             const int s = it % STAGES;
-            pipe_wait(&sh.empty[s], ((it / STAGES) - 1) & 1, abort, limit);
+            if (it >= STAGES) pipe_wait(&sh.empty[s], ((it / STAGES) - 1) & 1, abort, limit);
             // after an abort nothing more is loaded: the stage may not be free
             if (__any_sync(0xFFFFFFFFu, *abort != 0)) break;
             if (elect_one()) {
