@@ -190,38 +190,56 @@ __device__ __forceinline__ void apply_gate(float2 (&v)[4], const float2 (&g)[4],
         v[j] = __fmul2_rn(v[j], ACT ? make_float2(act_value(g[j].x, act), act_value(g[j].y, act)) : g[j]);
 }
 
-// v *= w + offset
+// A unit's factors in shared memory: written and read by its own thread alone (no
+// barrier), the halves of a unit apart so that a warp's accesses meet no bank twice.
+struct Kept {
+    float4 *base;
+    int units;
+    __device__ __forceinline__ void put(int which, int u, const float2 (&v)[4]) const {
+        base[(2 * which) * units + u] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+        base[(2 * which + 1) * units + u] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
+    }
+    __device__ __forceinline__ void multiply(int which, int u, float2 (&v)[4]) const {
+        const float4 lo = base[(2 * which) * units + u], hi = base[(2 * which + 1) * units + u];
+        v[0] = __fmul2_rn(v[0], make_float2(lo.x, lo.y));
+        v[1] = __fmul2_rn(v[1], make_float2(lo.z, lo.w));
+        v[2] = __fmul2_rn(v[2], make_float2(hi.x, hi.y));
+        v[3] = __fmul2_rn(v[3], make_float2(hi.z, hi.w));
+    }
+};
+
 template <typename T>
-__device__ __forceinline__ void apply_weight(const Raw<T> &r, float offset, float2 (&v)[4]) {
-    float2 w[4];
-    unpack<T>(r, w);
+__device__ __forceinline__ void weight_values(const Raw<T> &r, float offset, float2 (&v)[4]) {
+    unpack<T>(r, v);
 #pragma unroll
-    for (int j = 0; j < 4; j++) v[j] = __fmul2_rn(v[j], __fadd2_rn(w[j], both(offset)));
+    for (int j = 0; j < 4; j++) v[j] = __fadd2_rn(v[j], both(offset));
 }
 
 // QFMT 0: z in T; else z in that 4-bit format.  ACT: the gate goes through sigmoid or
-// tanh.  KEEP: the weights (and a gate that
-// serves every row) stay in registers from row to row, as they are stored, and the
-// next row is loaded ahead; without it (wide rows, which take the registers for
-// themselves) everything is loaded where it is used.
+// tanh.  KEEP: what every row is multiplied by (the weights, and a gate that serves
+// every row) waits in shared memory, ready, and the next row is loaded ahead; without
+// it (wide rows, which take the registers for themselves) everything is loaded where it
+// is used.
 //
-// At 21 M values in 26 us (8192 x 2560 BF16 at the copy rate) an SM lane has 45
-// issue slots per value, and this kernel takes about 40 of them (36.5 us, 71% of the
-// slots used): the arithmetic is in pairs (f32x2) and weights and gate stay packed.
-// Measured slower there: two units per thread (fewer instructions, but fewer warps:
-// 47 us); no row ahead and twice the CTAs (42 us); one warp per row without barriers
-// (its unrolled row is code run once per row, and the warps wait for instructions:
-// 47 us).
+// At 21 M values in 26 us (8192 x 2560 BF16 at the copy rate) an SM lane has 45 issue
+// slots per value.  So the arithmetic is in pairs (f32x2), a thread takes two units
+// where the row has them (the two reductions cost the same per thread), and the weights
+// are unpacked once per CTA: in registers they cost either the unpacking for every row
+// (one unit per thread: 46 slots, 36.4 us) or the warps that hide the loads.
 template <typename T, int PV, int MAXT, int MINB, bool KEEP, int MODE, int QFMT, bool ACT>
 __global__ void __launch_bounds__(MAXT, MINB) block_norm_kernel(const __grid_constant__ Args a) {
     __shared__ __align__(16) float part[4][32];
+    extern __shared__ float4 kept_units[];
+    // in this order: what the next kernel may read early is then complete
+    const int zero = fp4::wait_prior_grid_zero();
     pdl_allow_dependents();
-    const int D = a.D;
+    const int D = a.D, t = (int)threadIdx.x, threads = (int)blockDim.x;
+    const Kept kept = {kept_units, PV * threads};
     constexpr int KV = KEEP ? PV : 1;
-    Raw<T> y[PV], h[KV], g[KV], w_post[KV], w_pre[KV];
-    int m = blockIdx.x;
-    const bool one_gate = a.gate_rows >= a.M;
-    const float qg = QFMT == W4_FMT_NVFP4 ? __ldg(a.q.global_scale) : 1.0f;
+    Raw<T> y[PV], h[KV], g[KV];
+    int m = (int)blockIdx.x + zero;
+    const bool one_gate = KEEP && a.gate_rows >= a.M;
+    const float qg = QFMT == W4_FMT_NVFP4 ? fp4::load_scalar(a.q.global_scale) : 1.0f;
 #pragma unroll
     for (int p = 0; p < PV; p++) load_unit<T, MODE>(a.y, m * a.ldy, p, D, y[p]);
     if constexpr (KEEP) {
@@ -232,11 +250,24 @@ __global__ void __launch_bounds__(MAXT, MINB) block_norm_kernel(const __grid_con
         }
 #pragma unroll
         for (int p = 0; p < PV; p++) {
-            if (a.w_post) load_unit<T, MODE>(a.w_post, 0, p, D, w_post[p]);
-            if (a.w_pre) load_unit<T, MODE>(a.w_pre, 0, p, D, w_pre[p]);
+            float2 v[4];
+            if (a.w_post) {
+                weight_values<T>(fresh_unit<T, MODE>(a.w_post, zero, p, D), a.offset, v);
+                kept.put(0, p * threads + t, v);
+            }
+            if (a.w_pre) {
+                weight_values<T>(fresh_unit<T, MODE>(a.w_pre, zero, p, D), a.offset, v);
+                kept.put(1, p * threads + t, v);
+            }
+            if (a.gate && one_gate) {
+                float2 one[4] = {both(1.0f), both(1.0f), both(1.0f), both(1.0f)};
+                unpack<T>(g[p], v);
+                apply_gate<ACT>(one, v, a.gate_act);
+                kept.put(2, p * threads + t, one);
+            }
         }
     }
-    for (int i = threadIdx.x; i < 128; i += blockDim.x) part[i >> 5][i & 31] = 0.0f;
+    for (int i = t; i < 128; i += threads) part[i >> 5][i & 31] = 0.0f;
     __syncthreads();
     for (int row = 0;; row++) {
         float *sums = part[2 * (row & 1)];
@@ -260,23 +291,35 @@ __global__ void __launch_bounds__(MAXT, MINB) block_norm_kernel(const __grid_con
         const float2 scale2 = both(scale), res2 = both(a.residual_scale);
 #pragma unroll
         for (int p = 0; p < PV; p++) {
-            const int k = KEEP ? p : 0;
+            const int u = p * threads + t;
 #pragma unroll
             for (int j = 0; j < 4; j++) b[p][j] = __fmul2_rn(b[p][j], scale2);
             if (a.w_post) {
-                apply_weight<T>(KEEP ? w_post[k] : fresh_unit<T, MODE>(a.w_post, 0, p, D), a.offset, b[p]);
+                if constexpr (KEEP) {
+                    kept.multiply(0, u, b[p]);
+                } else {
+                    float2 v[4];
+                    weight_values<T>(fresh_unit<T, MODE>(a.w_post, zero, p, D), a.offset, v);
+#pragma unroll
+                    for (int j = 0; j < 4; j++) b[p][j] = __fmul2_rn(b[p][j], v[j]);
+                }
             }
             if (a.gate) {
-                float2 v[4];
-                unpack<T>(KEEP ? g[k] : fresh_unit<T, MODE>(a.gate, (m / a.gate_rows) * a.ldgate, p, D), v);
-                if (KEEP && !one_gate && next < a.M)
-                    load_unit<T, MODE>(a.gate, (next / a.gate_rows) * a.ldgate, p, D, g[p]);
-                apply_gate<ACT>(b[p], v, a.gate_act);
+                if (one_gate) {
+                    kept.multiply(2, u, b[p]);
+                } else {
+                    float2 v[4];
+                    unpack<T>(KEEP ? g[KEEP ? p : 0] : fresh_unit<T, MODE>(a.gate, (m / a.gate_rows) * a.ldgate, p, D),
+                              v);
+                    if (KEEP && next < a.M)
+                        load_unit<T, MODE>(a.gate, (next / a.gate_rows) * a.ldgate, p, D, g[KEEP ? p : 0]);
+                    apply_gate<ACT>(b[p], v, a.gate_act);
+                }
             }
             if (a.h) {
                 float2 v[4];
-                unpack<T>(KEEP ? h[k] : fresh_unit<T, MODE>(a.h, m * a.ldh, p, D), v);
-                if (KEEP && next < a.M) load_unit<T, MODE>(a.h, next * a.ldh, p, D, h[p]);
+                unpack<T>(KEEP ? h[KEEP ? p : 0] : fresh_unit<T, MODE>(a.h, m * a.ldh, p, D), v);
+                if (KEEP && next < a.M) load_unit<T, MODE>(a.h, next * a.ldh, p, D, h[KEEP ? p : 0]);
 #pragma unroll
                 for (int j = 0; j < 4; j++) b[p][j] = __ffma2_rn(res2, v[j], b[p][j]);
             }
@@ -288,15 +331,22 @@ __global__ void __launch_bounds__(MAXT, MINB) block_norm_kernel(const __grid_con
         const float2 r = both(rsqrtf(block_sum(ss.x + ss.y, sums + 32) * a.inv_D + a.eps));
 #pragma unroll
         for (int p = 0; p < PV; p++) {
+            const int u = p * threads + t;
 #pragma unroll
             for (int j = 0; j < 4; j++) b[p][j] = __fmul2_rn(b[p][j], r);
             if (a.w_pre) {
-                apply_weight<T>(KEEP ? w_pre[KEEP ? p : 0] : fresh_unit<T, MODE>(a.w_pre, 0, p, D), a.offset, b[p]);
+                if constexpr (KEEP) {
+                    kept.multiply(1, u, b[p]);
+                } else {
+                    float2 v[4];
+                    weight_values<T>(fresh_unit<T, MODE>(a.w_pre, zero, p, D), a.offset, v);
+#pragma unroll
+                    for (int j = 0; j < 4; j++) b[p][j] = __fmul2_rn(b[p][j], v[j]);
+                }
             }
             if constexpr (QFMT == 0) {
                 store_unit<T, MODE>(a.z, m * a.ldz, p, D, b[p]);
             } else {
-                const int u = p * (int)blockDim.x + (int)threadIdx.x;
                 const bool active = u < D / fp4::kUnit;
                 const float v[8] = {b[p][0].x, b[p][0].y, b[p][1].x, b[p][1].y,
                                     b[p][2].x, b[p][2].y, b[p][3].x, b[p][3].y};

@@ -33,24 +33,23 @@ int fp4_set_wait_limit(unsigned long long ns) {
 
 namespace {
 
-// Lanes of a pass over a matrix, 32 values each, rows padded to whole scale words.
-template <typename F>
-w4_status by_lanes(int rows, int K, F launch) {
-    const int per_row = (K / 32 + 3) / 4 * 4;
-    const long long blocks = ((long long)rows * per_row + 255) / 256;
-    if (blocks > kMaxBlocks) return W4_ERR_UNSUPPORTED;
-    launch((unsigned)blocks, per_row);
-    return launch_status();
+// Blocks of a pass over a matrix by lanes of 32 values, rows padded to whole scale words.
+bool lane_blocks(int rows, int K, int &per_row, unsigned &blocks) {
+    per_row = (K / 32 + 3) / 4 * 4;
+    const long long n = ((long long)rows * per_row + 255) / 256;
+    blocks = (unsigned)n;
+    return n <= kMaxBlocks;
 }
 
 template <typename T, int FMT>
 w4_status launch_quantize(const void *x, long long ldx, int rows, const fp4::Out &o, cudaStream_t st) {
     const T *p = reinterpret_cast<const T *>(x);
     const bool wide = (reinterpret_cast<uintptr_t>(x) | (uintptr_t)(ldx * sizeof(T))) % 32 == 0;
-    return by_lanes(rows, o.K, [&](unsigned blocks, int per_row) {
-        if (wide) fp4::quantize_kernel<T, FMT, true><<<blocks, 256, 0, st>>>(p, ldx, rows, per_row, o);
-        else fp4::quantize_kernel<T, FMT, false><<<blocks, 256, 0, st>>>(p, ldx, rows, per_row, o);
-    });
+    int per_row;
+    unsigned blocks;
+    if (!lane_blocks(rows, o.K, per_row, blocks)) return W4_ERR_UNSUPPORTED;
+    return launch_behind(wide ? fp4::quantize_kernel<T, FMT, true> : fp4::quantize_kernel<T, FMT, false>, blocks, 256,
+                         0, st, p, ldx, rows, per_row, o);
 }
 
 template <typename T>
@@ -71,16 +70,13 @@ w4_status quantize(const void *x, int type, long long ldx, int rows, int fmt, co
 template <typename T, int FMT>
 w4_status launch_dequantize(const w4_fp4 *a, void *out, long long ldo, cudaStream_t st) {
     T *p = reinterpret_cast<T *>(out);
-    const int tiles_k = fp4::scale_tiles_k(FMT, a->K);
     const bool wide = (reinterpret_cast<uintptr_t>(out) | (uintptr_t)(ldo * sizeof(T))) % 32 == 0;
-    return by_lanes(a->rows, a->K, [&](unsigned blocks, int per_row) {
-        if (wide)
-            fp4::dequantize_kernel<T, FMT, true><<<blocks, 256, 0, st>>>(a->codes, a->scales, a->global_scale, a->rows,
-                                                                         a->K, tiles_k, per_row, p, ldo);
-        else
-            fp4::dequantize_kernel<T, FMT, false><<<blocks, 256, 0, st>>>(a->codes, a->scales, a->global_scale,
-                                                                          a->rows, a->K, tiles_k, per_row, p, ldo);
-    });
+    int per_row;
+    unsigned blocks;
+    if (!lane_blocks(a->rows, a->K, per_row, blocks)) return W4_ERR_UNSUPPORTED;
+    return launch_behind(wide ? fp4::dequantize_kernel<T, FMT, true> : fp4::dequantize_kernel<T, FMT, false>, blocks,
+                         256, 0, st, a->codes, a->scales, a->global_scale, a->rows, a->K,
+                         fp4::scale_tiles_k(FMT, a->K), per_row, p, ldo);
 }
 
 template <typename T>
@@ -354,9 +350,8 @@ w4_status fp4_tile_scales(int fmt, int rows, int K, const uint8_t *row_scales, u
     const int tiles_k = fp4::scale_tiles_k(fmt, K);
     const long long blocks = ((long long)rows * tiles_k + 255) / 256;
     if (blocks > kMaxBlocks) return W4_ERR_UNSUPPORTED;
-    fp4::tile_scales_kernel<<<(unsigned)blocks, 256, 0, as_stream(stream)>>>(
-        row_scales, rows, K / (fmt == W4_FMT_MXFP4 ? 32 : 16), tiles_k, scales);
-    return launch_status();
+    return launch_behind(fp4::tile_scales_kernel, (unsigned)blocks, 256, 0, as_stream(stream), row_scales, rows,
+                         K / (fmt == W4_FMT_MXFP4 ? 32 : 16), tiles_k, scales);
 }
 
 w4_status w4a4_gemm(const w4_fp4 *w, const w4_fp4 *x, void *y, int out_type, long long ldy, unsigned flags,

@@ -24,6 +24,23 @@ namespace w4 {
 
 namespace fp4 {
 
+// Waits for the previous kernel on the stream and returns 0, which every address read
+// after it is to contain: loads marked read-only, and assembly that is not volatile,
+// may otherwise be moved up past the wait.
+__device__ __forceinline__ int wait_prior_grid_zero() {
+    int zero;
+    pdl_wait_prior_grid();
+    asm volatile("mov.b32 %0, 0;" : "=r"(zero) :: "memory");
+    return zero;
+}
+
+// One float, read where the program says.
+__device__ __forceinline__ float load_scalar(const float *p) {
+    float v;
+    asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+    return v;
+}
+
 constexpr int kUnit = 8;   // values of a lane of the norms: 16 bytes of a 16-bit type, 4 bytes of codes
 
 template <typename T> constexpr bool kIsHalf = false;

@@ -67,6 +67,25 @@ inline w4_status clear_status(int *d_status, cudaStream_t st) {
     return !d_status || cudaMemsetAsync(d_status, 0, sizeof(int), st) == cudaSuccess ? W4_OK : W4_ERR_CUDA;
 }
 
+// Launch of a kernel whose first step is to wait for the previous one on the stream
+// (pdl_wait_prior_grid): only its start overlaps that kernel's end.
+template <typename... P, typename... A>
+inline w4_status launch_behind(void (*kernel)(P...), unsigned grid, unsigned threads, size_t smem, cudaStream_t st,
+                               A... args) {
+    if (smem > 48 * 1024 - 1024 && !set_smem_limit(reinterpret_cast<const void *>(kernel), smem)) return W4_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid, 1, 1);
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...) == cudaSuccess ? launch_status() : W4_ERR_CUDA;
+}
+
 // This translation unit's sticky error word: added to *out if that is 0.
 inline w4_status take_device_error(int *out, int clear) {
     int v = 0;

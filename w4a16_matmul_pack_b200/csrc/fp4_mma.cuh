@@ -138,7 +138,7 @@ struct Factor {
     double d;
     bool wide;
     __device__ __forceinline__ Factor(const float *ga, const float *gb) {
-        d = (ga ? (double)__ldg(ga) : 1.0) * (gb ? (double)__ldg(gb) : 1.0);
+        d = (ga ? (double)fp4::load_scalar(ga) : 1.0) * (gb ? (double)fp4::load_scalar(gb) : 1.0);
         f = (float)d;
         const double m = fabs(d);
         wide = !(d == 0.0 || (m >= 0x1p-126 && m < 0x1p128));

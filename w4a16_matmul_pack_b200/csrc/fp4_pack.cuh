@@ -71,14 +71,16 @@ __device__ __forceinline__ void values8(const uint32_t *w, float (&v)[8]) {
 template <typename T, int FMT, bool WIDE>
 __global__ void __launch_bounds__(256) quantize_kernel(const T *__restrict__ x, long long ldx, int rows, int per_row,
                                                        const Out o) {
+    // in this order: what the next kernel may read early is then complete
+    const int zero = wait_prior_grid_zero();
     pdl_allow_dependents();
-    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+    const long long i = (long long)blockIdx.x * 256 + threadIdx.x + zero;
     const long long row = i < 0x80000000ll ? (long long)((uint32_t)i / (uint32_t)per_row) : i / per_row;
     const int u = (int)(i - row * per_row);
     const bool active = row < rows && u * 32 < o.K;
     constexpr int WORDS = 8 * sizeof(T), LOAD = WIDE ? 8 : 4;
     uint32_t w[WORDS];
-    const float g = FMT == W4_FMT_NVFP4 ? __ldg(o.global_scale) : 1.0f;
+    const float g = FMT == W4_FMT_NVFP4 ? load_scalar(o.global_scale) : 1.0f;
     if (active) {
         const T *p = x + row * ldx + (long long)u * 32;
 #pragma unroll
@@ -125,7 +127,7 @@ __global__ void __launch_bounds__(256) dequantize_kernel(const uint8_t *__restri
                                                          const uint8_t *__restrict__ scales,
                                                          const float *__restrict__ gscale, int rows, int K, int tiles_k,
                                                          int per_row, T *__restrict__ out, long long ldo) {
-    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+    const long long i = (long long)blockIdx.x * 256 + threadIdx.x + wait_prior_grid_zero();
     const long long row = i < 0x80000000ll ? (long long)((uint32_t)i / (uint32_t)per_row) : i / per_row;
     const int u = (int)(i - row * per_row);
     if (row >= rows || u * 32 >= K) return;
@@ -133,7 +135,7 @@ __global__ void __launch_bounds__(256) dequantize_kernel(const uint8_t *__restri
     uint32_t c[4];
     load_words<4>(codes + row * (K / 2) + (long long)u * 16, c);
     const uint8_t *sp = scales + scale_word_offset((int)row, u * NB / 4, tiles_k) + (u * NB) % 4;
-    const float g = FMT == W4_FMT_NVFP4 ? __ldg(gscale) : 1.0f;
+    const float g = FMT == W4_FMT_NVFP4 ? load_scalar(gscale) : 1.0f;
     uint32_t w[WORDS];
 #pragma unroll
     for (int e = 0; e < 4; e++) {
@@ -165,7 +167,7 @@ __global__ void __launch_bounds__(256) dequantize_kernel(const uint8_t *__restri
 // last word of a row).
 __global__ void __launch_bounds__(256) tile_scales_kernel(const uint8_t *__restrict__ src, int rows, int per_row,
                                                           int tiles_k, uint8_t *__restrict__ dst) {
-    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+    const long long i = (long long)blockIdx.x * 256 + threadIdx.x + wait_prior_grid_zero();
     const long long row = i / tiles_k;
     if (row >= rows) return;
     const int word = (int)(i - row * tiles_k);

@@ -18,12 +18,12 @@ int norm_device_error(int *out, int clear) { return take_device_error(out, clear
 namespace {
 
 template <typename T, int PV, int MAXT, int MINB, bool KEEP, int QFMT, bool ACT>
-void launch_block(const norm::Args &a, int mode, int grid, int threads, cudaStream_t st) {
+w4_status launch_block(const norm::Args &a, int mode, int grid, int threads, cudaStream_t st) {
     constexpr int ODD = QFMT != 0 ? norm::SCALAR : norm::STRIDED;
-    if (mode == norm::VECTOR)
-        norm::block_norm_kernel<T, PV, MAXT, MINB, KEEP, norm::VECTOR, QFMT, ACT><<<grid, threads, 0, st>>>(a);
-    else
-        norm::block_norm_kernel<T, PV, MAXT, MINB, KEEP, ODD, QFMT, ACT><<<grid, threads, 0, st>>>(a);
+    return launch_behind(mode == norm::VECTOR
+                             ? norm::block_norm_kernel<T, PV, MAXT, MINB, KEEP, norm::VECTOR, QFMT, ACT>
+                             : norm::block_norm_kernel<T, PV, MAXT, MINB, KEEP, ODD, QFMT, ACT>,
+                         (unsigned)grid, (unsigned)threads, KEEP ? (size_t)threads * PV * 96 : 0, st, a);
 }
 
 // Threads per SM that the register use leaves room for (64 registers each); CTAs beyond
@@ -36,14 +36,14 @@ w4_status launch_norm(const norm::Args &a, int mode, cudaStream_t st) {
     const int units = (a.D + fp4::kUnit - 1) / fp4::kUnit;
     int sms = 0;
     if (device_sms(sms) != W4_OK) return W4_ERR_CUDA;
-    const int pv = units <= 512 ? 1 : units <= 1024 ? 2 : 4;
+    // a batch with no more rows than SMs has threads to spare for a shorter row (one row
+    // of 2560: one unit per thread 2.7 us, two 3.1 us)
+    const int pv = units <= 32 || (units <= 512 && a.M <= sms) ? 1 : units <= 1024 ? 2 : 4;
     const int threads = ((units + pv - 1) / pv + 31) / 32 * 32;
     const int grid = std::min(a.M, sms * std::max(1, kResident / threads));
-    constexpr bool half = sizeof(T) == 2;
-    if (pv == 1) launch_block<T, 1, 512, half ? 2 : 1, true, QFMT, ACT>(a, mode, grid, threads, st);
-    else if (pv == 2) launch_block<T, 2, 512, 1, half, QFMT, ACT>(a, mode, grid, threads, st);
-    else launch_block<T, 4, 1024, 1, false, QFMT, ACT>(a, mode, grid, threads, st);
-    return launch_status();
+    if (pv == 1) return launch_block<T, 1, 512, sizeof(T) == 2 ? 2 : 1, true, QFMT, ACT>(a, mode, grid, threads, st);
+    if (pv == 2) return launch_block<T, 2, 512, sizeof(T) == 2 ? 2 : 1, true, QFMT, ACT>(a, mode, grid, threads, st);
+    return launch_block<T, 4, 1024, 1, false, QFMT, ACT>(a, mode, grid, threads, st);
 }
 
 template <typename T, int QFMT>
