@@ -189,8 +189,13 @@ w4_status launch_pair(const w4_fp4 *w, const w4_fp4 *x, void *y, long long ldy, 
         return W4_ERR_CUDA;
     constexpr size_t smem = sizeof(pair::Shared<FMT, NT>) + 1024;
     static_assert(smem <= 227 * 1024, "shared memory of the product");
-    auto kernel = pair::gemm_kernel<FMT, NT>;
+    // y leaves as TMA boxes where its rows start on 16 bytes and, since a box is clipped
+    // to the tensor in units of 16 bytes, end on them
+    const bool tma = rows16(ldy, out_type) && rows16(w->rows, out_type);
+    auto kernel = tma ? pair::gemm_kernel<FMT, NT, true> : pair::gemm_kernel<FMT, NT, false>;
     if (!set_smem_limit(reinterpret_cast<const void *>(kernel), smem)) return W4_ERR_CUDA;
+    CUtensorMap ymap = xmap;   // not read without tma
+    if (tma && !output_map(ymap, y, x->rows, w->rows, ldy, out_type)) return W4_ERR_CUDA;
     pair::Params p;
     p.gx = FMT == W4_FMT_NVFP4 ? x->global_scale : nullptr;
     p.gw = FMT == W4_FMT_NVFP4 ? w->global_scale : nullptr;
@@ -199,10 +204,6 @@ w4_status launch_pair(const w4_fp4 *w, const w4_fp4 *x, void *y, long long ldy, 
     p.out.rows = x->rows;
     p.out.cols = w->rows;
     p.out.type = out_type;
-    // a box is clipped to the tensor in units of 16 bytes, so a row must end on one
-    p.out.tma = rows16(ldy, out_type) && rows16(w->rows, out_type);
-    CUtensorMap ymap = xmap;   // not read without p.out.tma
-    if (p.out.tma && !output_map(ymap, y, x->rows, w->rows, ldy, out_type)) return W4_ERR_CUDA;
     p.K = x->K;
     p.early_w = early_w;
     p.tiles_m = (x->rows + 2 * BM - 1) / (2 * BM);

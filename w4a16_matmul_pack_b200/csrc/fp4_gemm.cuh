@@ -117,7 +117,8 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
 
-template <int FMT, int NT>
+// TMA: y leaves as TMA boxes (its rows start and end on 16 bytes).
+template <int FMT, int NT, bool TMA>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
                 const __grid_constant__ CUtensorMap sxmap, const __grid_constant__ CUtensorMap swmap,
@@ -281,10 +282,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (lane == 0) arrive_cluster(empty);
                 }
                 apply_factor(fac, v);
-                store_rows(p.out, &ymap, sh.out[warp - kEpiWarp0], m0, n0 + c * CHUNK, v);
+                store_rows<TMA>(p.out, &ymap, sh.out[warp - kEpiWarp0], m0, n0 + c * CHUNK, v);
             }
         }
-        store_rows_done();
+        if (TMA) store_rows_done();
         __syncwarp();
     }
 
