@@ -766,7 +766,7 @@ def run_reference(args, world, rank):
 # one launch of the dominant kernel, w4::gemv_nvfp4_m1_grouped_kernel, on the
 # five sweep matrices, with the SHA-256 of the kernel sources it was measured
 # on.  The bench reports it only while those sources are unchanged.
-TRAFFIC = {"bytes": 41407488, "source_sha256": "3069d169f809520928beaa43fc45705d26d85d62d20ae0692f00e798c204e9db"}
+TRAFFIC = {"bytes": 41390592, "source_sha256": "185c123a5625a1e35afeb5b243fdaacdfc1ebab758a1ea24285c102e61a40691"}
 TRAFFIC_SOURCES = ("common.cuh", "gemv_tc.cuh", "gemv_m1.cuh", "w4a16.cu")
 
 

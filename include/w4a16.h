@@ -412,10 +412,12 @@ w4_status w4a4_gemm(const w4_fp4 *w, const w4_fp4 *x, void *y, int out_type, lon
 
 /*
  * w4a4_linear -- fp4_quantize of x to w's format, then w4a4_gemm, in one call:
- * the linear layer with 4-bit activations.
+ * the linear layer with 4-bit activations, the same bits as the two calls.  Up to
+ * 16 tokens are quantised inside the product.
  *   x, type, ldx, scale_rule, global_scale (of x), d_status  as for fp4_quantize.
- *   workspace >= w4a4_workspace_bytes(w, M) bytes: the 4-bit x.  Calls whose work
- *             may overlap need workspaces of their own.
+ *   workspace >= w4a4_workspace_bytes(w, M) bytes: the 4-bit x (0 up to 16 tokens:
+ *             NULL allowed then).  Calls whose work may overlap need workspaces of
+ *             their own.
  */
 w4_status w4a4_linear(const w4_fp4 *w, const void *x, int type, long long ldx, int M, int scale_rule,
                       const float *global_scale, void *y, int out_type, long long ldy, void *workspace,

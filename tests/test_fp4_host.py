@@ -90,21 +90,26 @@ def test_product_refusals(lib):
 
 def test_linear_refusals(lib):
     w = operand()
-    need = lib.w4a4_workspace_bytes(ctypes.byref(w), 3)
-    assert need >= 3 * 32 + 512
-    assert lib.w4a4_workspace_bytes(ctypes.byref(w), 0) == 0
-    for M in (1, 3, 77, 129, 1000):       # the binding's own arithmetic
+    need = lib.w4a4_workspace_bytes(ctypes.byref(w), 17)
+    assert need >= 17 * 32 + 512
+    assert lib.w4a4_workspace_bytes(ctypes.byref(w), 0) == lib.w4a4_workspace_bytes(ctypes.byref(w), 16) == 0
+    for M in (1, 16, 17, 77, 129, 1000):       # the binding's own arithmetic
         for fmt, K in ((5, 64), (5, 2592), (1, 96)):
             c = operand(fmt, 8, K, g=16 if fmt == 1 else None)
-            assert W4.w4a4_workspace_bytes(c, M) == lib.w4a4_workspace_bytes(ctypes.byref(c), M) > 0
+            assert W4.w4a4_workspace_bytes(c, M) == lib.w4a4_workspace_bytes(ctypes.byref(c), M)
 
-    def call(w=w, x=P(16), type=0, ldx=64, M=3, rule=0, g=None, y=P(16), out=0, ldy=8, ws=P(256), n=need):
+    def call(w=w, x=P(16), type=0, ldx=64, M=17, rule=0, g=None, y=P(16), out=0, ldy=8, ws=P(256), n=need):
         return lib.w4a4_linear(ctypes.byref(w), x, type, ldx, M, rule, g, y, out, ldy, ws, n, None, None)
     assert call(x=None) == ARG and call(M=0) == ARG and call(ldx=60) == ARG and call(type=5) == ARG
     assert call(ws=None) == WORKSPACE and call(n=need - 1) == WORKSPACE
     assert call(y=None) == ARG and call(out=3) == ARG and call(ldy=5) == ARG and call(rule=4) == ARG
     assert call(x=P(24)) == ALIGN and call(ldx=66) == ALIGN and call(ws=P(264)) == ALIGN and call(y=P(8)) == ALIGN
-    assert call(w=operand(fmt=1, g=16)) == ARG                  # NVFP4 x without a global scale
+    assert call(w=operand(fmt=1, g=16), n=1 << 20) == ARG       # NVFP4 x without a global scale
+    few = dict(M=16, ws=None, n=0)                              # no workspace, the same refusals
+    assert call(**few, x=None) == ARG and call(**few, ldx=60) == ARG and call(**few, type=5) == ARG
+    assert call(**few, y=None) == ARG and call(**few, out=3) == ARG and call(**few, ldy=5) == ARG and call(**few, rule=4) == ARG
+    assert call(**few, x=P(24)) == ALIGN and call(**few, ldx=66) == ALIGN and call(**few, y=P(8)) == ALIGN
+    assert call(**few, w=operand(fmt=1, g=16)) == ARG
 
 
 def test_norm_refusals(lib):

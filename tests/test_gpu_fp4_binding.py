@@ -47,8 +47,8 @@ def test_product():
     refused(lambda: W4.w4a4_gemm(w, q, flags=4), W4.W4Error)
     refused(lambda: W4.w4a4_linear(w, x(K=96)))
     refused(lambda: W4.w4a4_linear(w, x(M=0)), W4.W4Error)
-    ws = torch.empty(W4.w4a4_workspace_bytes(w, 4) - 16, dtype=torch.uint8, device="cuda")
-    refused(lambda: W4.w4a4_linear(w, x(), workspace=ws), W4.W4Error)
+    ws = torch.empty(W4.w4a4_workspace_bytes(w, 40) - 16, dtype=torch.uint8, device="cuda")
+    refused(lambda: W4.w4a4_linear(w, x(40), workspace=ws), W4.W4Error)
     nv = W4.fp4_quantize(x(8), "nvfp4", global_scale=torch.ones(1, device="cuda"))
     refused(lambda: W4.w4a4_linear(nv, x()), W4.W4Error)                      # no global scale of x
     refused(lambda: W4.w4a4_gemm(nv, q), W4.W4Error)                          # two formats

@@ -1,0 +1,56 @@
+"""Failure detection of the W4A4 products without a GPU fault: with a wait limit so
+short that the first waits expire, a call records W4_ERR_TIMEOUT in the sticky word
+and returns; with the default limit restored the next call is right and records
+nothing."""
+import time
+
+import pytest
+import torch
+
+import w4a16_matmul_pack_b200 as W4
+
+pytestmark = pytest.mark.gpu
+
+W4_ERR_TIMEOUT = 6
+
+
+@pytest.fixture(autouse=True)
+def default_limit_after():
+    W4.w4_device_error(clear=True)
+    yield
+    W4.set_wait_limit(0)
+    W4.w4_device_error(clear=True)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("M,N,K", [(1, 2560, 2560), (9, 256, 9728), (100, 512, 2560), (300, 1000, 4096), (2048, 2560, 2560)])
+def test_expired_waits_are_reported_and_pass(fmt, M, N, K):
+    g = torch.tensor([0.002], device="cuda") if fmt == "nvfp4" else None
+    gen = torch.Generator().manual_seed(M)
+    x = W4.fp4_quantize(torch.randn(M, K, generator=gen).cuda(), fmt, global_scale=g)
+    w = W4.fp4_quantize(torch.randn(N, K, generator=gen).cuda(), fmt, global_scale=g)
+    want = W4.w4a4_gemm(w, x, out_dtype=torch.float32)
+    torch.cuda.synchronize()
+    W4.set_wait_limit(1)                      # 1 ns: the first wait that does not pass at once expires
+    t = time.monotonic()
+    W4.w4a4_gemm(w, x, out_dtype=torch.float32)
+    torch.cuda.synchronize()
+    assert time.monotonic() - t < 30          # every wait of the way out is bounded
+    assert W4.w4_device_error(clear=True) == W4_ERR_TIMEOUT
+    W4.set_wait_limit(0)
+    got = W4.w4a4_gemm(w, x, out_dtype=torch.float32)
+    torch.cuda.synchronize()
+    assert W4.w4_device_error(clear=True) == 0
+    assert torch.equal(got, want)
+
+
+def test_nonfinite_inputs_reach_the_sticky_word_from_every_kernel():
+    """The norms, the quantiser and the weight packers share one sticky word."""
+    bad = torch.full((2, 64), float("inf"), device="cuda")
+    for call in (lambda: W4.fp4_quantize(bad), lambda: W4.block_norm(bad, quantize="mxfp4"),
+                 lambda: W4.pack_nvfp4(bad.to(torch.bfloat16))):
+        assert W4.w4_device_error(clear=True) == 0
+        call()
+        assert W4.w4_device_error(clear=False) == 5
+        assert W4.w4_device_error(clear=True) == 5
+        assert W4.w4_device_error(clear=True) == 0

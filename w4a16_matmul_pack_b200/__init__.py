@@ -371,6 +371,7 @@ def w4a16_gemm(w: PackedWeights, x: torch.Tensor, *, want_f32: bool = True, want
 _TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _FP4_FMTS = {"mxfp4": FMT_MXFP4, "nvfp4": FMT_NVFP4, FMT_MXFP4: FMT_MXFP4, FMT_NVFP4: FMT_NVFP4}
 _GATES = {"none": 0, "sigmoid": 1, "tanh": 2}
+_FUSED_TOKENS = 16   # tokens up to which w4a4_linear needs no workspace
 _pack_fp4 = struct.Struct("@iiiPPP").pack                              # w4_fp4
 _pack_norm = struct.Struct("@iiiPPPPPqqqiiffffPqPqiiPPPP").pack        # w4_norm
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -591,7 +592,7 @@ def w4a4_gemm(w: Fp4Tensor, x: Fp4Tensor, *, out_dtype: torch.dtype = torch.bflo
 
 def w4a4_workspace_bytes(w: Fp4Tensor, M: int) -> int:
     """Bytes of workspace w4a4_linear needs (as w4a4_workspace_bytes in include/w4a16.h)."""
-    return ((M * (w.K // 2) + 255) & ~255) + fp4_scale_bytes(w.fmt, M, w.K) if M >= 1 else 0
+    return ((M * (w.K // 2) + 255) & ~255) + fp4_scale_bytes(w.fmt, M, w.K) if M > _FUSED_TOKENS else 0
 
 
 def w4a4_linear(w: Fp4Tensor, x: torch.Tensor, *, global_scale: Optional[torch.Tensor] = None,
@@ -611,16 +612,18 @@ def w4a4_linear(w: Fp4Tensor, x: torch.Tensor, *, global_scale: Optional[torch.T
     if out is None:
         out = _new(M, w.rows, out_dtype, device)
     yptr, yld, _, _ = _rows(out, "out", dev, M, w.rows)
-    if workspace is None:
-        need = w4a4_workspace_bytes(w, M)
-        workspace = torch.empty_strided((need,), (1,), dtype=torch.uint8, device=device)
-    else:
+    wptr = need = 0
+    if workspace is not None:
         _cuda(workspace, "workspace", torch.uint8)
-        need = workspace.numel()
+        wptr, need = workspace.data_ptr(), workspace.numel()
         if workspace.get_device() != dev:
             raise ValueError(f"workspace must be on cuda:{dev}, got {workspace.device}")
+    elif M > _FUSED_TOKENS:
+        need = w4a4_workspace_bytes(w, M)
+        workspace = torch.empty_strided((need,), (1,), dtype=torch.uint8, device=device)
+        wptr = workspace.data_ptr()
     _call(dev, stream, "w4a4_linear", lib().w4a4_linear, w._c, ptr, _type(x, "x"), ld, M, scale_rule, g, yptr,
-          _type(out, "out"), yld, workspace.data_ptr(), need, _vector(d_status, "d_status", torch.int32, dev, 1))
+          _type(out, "out"), yld, wptr, need, _vector(d_status, "d_status", torch.int32, dev, 1))
     return out
 
 

@@ -100,37 +100,53 @@ bool codes_map(CUtensorMap &map, const uint8_t *codes, int rows, int K, int box_
                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int FMT, int NT>
-w4_status launch_skinny(const w4_fp4 *w, const w4_fp4 *x, void *y, long long ldy, int out_type, int splits,
-                        bool early_w, cudaStream_t st) {
+// x of at most 16 tokens that the product quantises itself.
+struct PlainX {
+    const void *x;
+    long long ldx;
+    int rows, type, ceil_rule;
+    const float *global_scale;
+    int *d_status;
+};
+
+template <int FMT, int NT, typename T>
+w4_status launch_skinny(const w4_fp4 *w, const w4_fp4 *x, const PlainX &plain, void *y, long long ldy, int out_type,
+                        int splits, bool early_w, cudaStream_t st) {
     using namespace fgemm;
+    constexpr bool fused = skinny::kFused<T>;
+    const int M = fused ? plain.rows : x->rows;
     CUtensorMap wmap, xmap;
-    if (!codes_map(wmap, w->codes, w->rows, w->K, BM) || !codes_map(xmap, x->codes, x->rows, x->K, NT))
-        return W4_ERR_CUDA;
+    if (!codes_map(wmap, w->codes, w->rows, w->K, BM)) return W4_ERR_CUDA;
+    xmap = wmap;   // not read when x is quantised here
+    if (!fused && !codes_map(xmap, x->codes, M, x->K, NT)) return W4_ERR_CUDA;
     constexpr size_t smem = sizeof(skinny::Shared<FMT, NT>) + 1024;
     static_assert(smem <= 227 * 1024, "shared memory of the product");
-    auto kernel = skinny::gemm_kernel<FMT, NT>;
+    auto kernel = skinny::gemm_kernel<FMT, NT, T>;
     if (!set_smem_limit(reinterpret_cast<const void *>(kernel), smem)) return W4_ERR_CUDA;
-    skinny::Params p;
+    skinny::Params p = {};
     p.sfw = w->scales;
-    p.sfx = x->scales;
+    p.sfx = fused ? nullptr : x->scales;
     p.gw = FMT == W4_FMT_NVFP4 ? w->global_scale : nullptr;
-    p.gx = FMT == W4_FMT_NVFP4 ? x->global_scale : nullptr;
+    p.gx = FMT == W4_FMT_NVFP4 ? (fused ? plain.global_scale : x->global_scale) : nullptr;
     p.y = y;
     p.ldy = ldy;
     p.N = w->rows;
-    p.M = x->rows;
-    p.K = x->K;
+    p.M = M;
+    p.K = w->K;
     p.tiles_n = (w->rows + BM - 1) / BM;
-    p.tiles_k = fp4::scale_tiles_k(FMT, x->K);
+    p.tiles_k = fp4::scale_tiles_k(FMT, w->K);
+    p.x = plain.x;
+    p.ldx = plain.ldx;
+    p.ceil_rule = plain.ceil_rule;
+    p.d_status = plain.d_status;
     p.splits = splits;
     p.out_type = out_type;
     p.early_w = early_w;
-    const long long blocks = (long long)p.tiles_n * ((x->rows + NT - 1) / NT) * splits;
+    const long long blocks = (long long)p.tiles_n * ((M + NT - 1) / NT) * splits;
     if (blocks > kMaxBlocks) return W4_ERR_UNSUPPORTED;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)blocks, 1, 1);
-    cfg.blockDim = dim3(skinny::kThreads, 1, 1);
+    cfg.blockDim = dim3(skinny::kThreads<T>, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     // The kernel waits for the previous one on the stream before it reads x or writes
@@ -246,12 +262,26 @@ int slices(long long tiles, int stages, int nt, int sms) {
     return best;
 }
 
-template <int FMT, int NT>
+template <int FMT, int NT, typename T = fgemm::skinny::Quantised>
 w4_status few_tokens(const w4_fp4 *w, const w4_fp4 *x, void *y, long long ldy, int out_type, bool early_w, int sms,
-                     cudaStream_t st) {
+                     cudaStream_t st, const PlainX &plain = {}) {
     const long long tiles = (w->rows + fgemm::BM - 1) / fgemm::BM;
     const int s = slices(tiles, (w->K + fgemm::BK - 1) / fgemm::BK, NT, sms);
-    return launch_skinny<FMT, NT>(w, x, y, ldy, out_type, s, early_w, st);
+    return launch_skinny<FMT, NT, T>(w, x, plain, y, ldy, out_type, s, early_w, st);
+}
+
+// The linear layer of at most kFusedTokens tokens in one kernel.
+constexpr int kFusedTokens = 16;
+
+template <int FMT>
+w4_status fused_linear(const w4_fp4 *w, const PlainX &x, void *y, long long ldy, int out_type, cudaStream_t st) {
+    int sms = 0;
+    if (device_sms(sms) != W4_OK) return W4_ERR_CUDA;
+    switch (x.type) {
+    case W4_TYPE_BF16: return few_tokens<FMT, 16, __nv_bfloat16>(w, nullptr, y, ldy, out_type, false, sms, st, x);
+    case W4_TYPE_F16: return few_tokens<FMT, 16, __half>(w, nullptr, y, ldy, out_type, false, sms, st, x);
+    default: return few_tokens<FMT, 16, float>(w, nullptr, y, ldy, out_type, false, sms, st, x);
+    }
 }
 
 // Width of a prompt's tiles: the least of launch + waves x (stages x time per stage +
@@ -364,7 +394,7 @@ w4_status w4a4_gemm(const w4_fp4 *w, const w4_fp4 *x, void *y, int out_type, lon
 }
 
 size_t w4a4_workspace_bytes(const w4_fp4 *w, int M) {
-    if (check_operand(w) != W4_OK || M < 1) return 0;
+    if (check_operand(w) != W4_OK || M <= kFusedTokens) return 0;
     return linear_scales_at(M, w->K) + fp4_scale_bytes(w->fmt, M, w->K);
 }
 
@@ -374,13 +404,25 @@ w4_status w4a4_linear(const w4_fp4 *w, const void *x, int type, long long ldx, i
     w4_status s = check_operand(w);
     if (s != W4_OK) return s;
     if (M < 1 || !x || !is_type(type) || ldx < w->K) return W4_ERR_ARG;
+    cudaStream_t st = as_stream(stream);
+    if (M <= kFusedTokens) {
+        // y's and x's arguments, checked as for an operand in w's own codes
+        const w4_fp4 q = {w->fmt, M, w->K, w->codes, w->scales, global_scale};
+        if ((s = check_quantised(M, w->K, w->fmt, scale_rule, global_scale, q.codes, q.scales, d_status)) != W4_OK)
+            return s;
+        if ((s = check_product(w, &q, y, ldy, out_type)) != W4_OK) return s;
+        if (!aligned16(x) || !rows16(ldx, type)) return W4_ERR_ALIGN;
+        if (clear_status(d_status, st) != W4_OK) return W4_ERR_CUDA;
+        const PlainX p = {x, ldx, M, type, scale_rule == W4_MX_SCALE_CEIL, global_scale, d_status};
+        return w->fmt == W4_FMT_MXFP4 ? fused_linear<W4_FMT_MXFP4>(w, p, y, ldy, out_type, st)
+                                      : fused_linear<W4_FMT_NVFP4>(w, p, y, ldy, out_type, st);
+    }
     if (!workspace || workspace_bytes < w4a4_workspace_bytes(w, M)) return W4_ERR_WORKSPACE;
     uint8_t *codes = reinterpret_cast<uint8_t *>(workspace), *scales = codes + linear_scales_at(M, w->K);
     const w4_fp4 q = {w->fmt, M, w->K, codes, scales, global_scale};
     if ((s = check_quantised(M, w->K, w->fmt, scale_rule, global_scale, codes, scales, d_status)) != W4_OK) return s;
     if ((s = check_product(w, &q, y, ldy, out_type)) != W4_OK) return s;
     if (!aligned16(x) || !rows16(ldx, type)) return W4_ERR_ALIGN;
-    cudaStream_t st = as_stream(stream);
     if (clear_status(d_status, st) != W4_OK) return W4_ERR_CUDA;
     s = quantize(x, type, ldx, M, w->fmt,
                  quantised_out(w->K, w->fmt, scale_rule, global_scale, codes, scales, d_status), st);

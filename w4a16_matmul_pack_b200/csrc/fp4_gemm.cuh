@@ -197,7 +197,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         // no load may land and no commit arrive after this CTA has left: the first CTA
         // waits for both CTAs' loads, each for the MMAs' arrivals on its own barriers,
         // and both meet in the cluster barrier at the end
-        if (rank == 0 && is_w) drain_ring(sh.full, STAGES, it);
+        if (rank == 0 && is_w) {
+            // (after an abort a stage may lack the loads the other CTA or warp did not issue:
+            // one full wait, and what was issued has landed)
+            for (int i = max(0, it - STAGES); i < it; i++)
+                if (!mbar_wait_bounded(&sh.full[i % STAGES], (uint32_t)((i / STAGES) & 1))) break;
+        }
         for (int i = max(0, it - STAGES); i < it; i++)
             pipe_wait(&sh.empty[i % STAGES], (i / STAGES) & 1, abort, limit);
         __syncwarp();

@@ -8,61 +8,6 @@ namespace w4 {
 
 namespace fp4 {
 
-// 32 or 16 consecutive bytes.
-template <int WORDS>
-__device__ __forceinline__ void load_words(const void *p, uint32_t *w) {
-    if constexpr (WORDS == 8)
-        asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
-                     : "l"(p));
-    else
-        asm volatile("ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(p));
-}
-template <int WORDS>
-__device__ __forceinline__ void store_words(void *p, const uint32_t *w) {
-    if constexpr (WORDS == 8)
-        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
-                     ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                     : "memory");
-    else
-        asm volatile("st.global.v4.b32 [%0], {%1, %2, %3, %4};"
-                     ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
-}
-
-// Largest magnitude of n words of T, as binary32 bits.
-template <typename T>
-__device__ __forceinline__ uint32_t absmax_words(const uint32_t *w, int n) {
-    uint32_t m = 0;
-    if constexpr (sizeof(T) == 4) {
-#pragma unroll
-        for (int i = 0; i < n; i++) m = max(m, w[i] & 0x7FFFFFFFu);
-        return m;
-    } else {
-#pragma unroll
-        for (int i = 0; i < n; i++) m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);
-        m = max(m & 0xFFFFu, m >> 16);
-        if constexpr (sizeof(T) == 2 && !kIsHalf<T>)
-            return m << 16;
-        else
-            return __float_as_uint(__half2float(__ushort_as_half((unsigned short)m))) & 0x7FFFFFFFu;
-    }
-}
-
-// Eight values from the words at w.
-template <typename T>
-__device__ __forceinline__ void values8(const uint32_t *w, float (&v)[8]) {
-#pragma unroll
-    for (int j = 0; j < 8; j++) {
-        if constexpr (sizeof(T) == 4) v[j] = __uint_as_float(w[j]);
-        else if constexpr (!kIsHalf<T>) v[j] = j % 2 ? bf16_hi(w[j / 2]) : bf16_lo(w[j / 2]);
-        else {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[j / 2]));
-            v[j] = j % 2 ? f.y : f.x;
-        }
-    }
-}
-
 // One lane per 32 values, per_row lanes per row (K / 32 and up to three more, whose
 // scales are the padding of the last word).  A lane of eight values (as the norms
 // write) would spend as many instructions on its block's scale and its addresses as on
@@ -89,25 +34,10 @@ __global__ void __launch_bounds__(256) quantize_kernel(const T *__restrict__ x, 
 #pragma unroll
         for (int j = 0; j < WORDS; j++) w[j] = 0u;
     }
-    constexpr int NB = 32 / Format<FMT>::BLOCK, BW = WORDS / NB;   // blocks of the lane, words of a block
-    const int lane = threadIdx.x & 31;
-    uint32_t word = 0, c[4];
-    bool bad = false;
-#pragma unroll
-    for (int b = 0; b < NB; b++) {
-        const uint32_t amax = absmax_words<T>(w + b * BW, BW);
-        float f;
-        word |= block_scale<FMT>(amax, g, o.ceil_rule, f) << (8 * ((NB * lane + b) & 3));
-        bad = bad || amax >= 0x7F800000u;
-#pragma unroll
-        for (int e = 0; e < 4 / NB; e++) {
-            float v[8];
-            values8<T>(w + b * BW + e * (WORDS / 4), v);
-            c[b * (4 / NB) + e] = amax >= 0x7F800000u ? 0u : pack_e2m1x8(v, f);
-        }
-    }
-    word |= __shfl_xor_sync(0xFFFFFFFFu, word, 1);
-    if (NB == 1) word |= __shfl_xor_sync(0xFFFFFFFFu, word, 2);
+    constexpr int NB = 32 / Format<FMT>::BLOCK;
+    uint32_t c[4];
+    bool bad;
+    const uint32_t word = quantize32<T, FMT>(w, g, o.ceil_rule, c, bad);
     if (row >= rows) return;
     if (active) store_words<4>(o.codes + row * (o.K / 2) + (long long)u * 16, c);
     if (u * NB % 4 == 0 && u * NB / 4 < o.tiles_k)

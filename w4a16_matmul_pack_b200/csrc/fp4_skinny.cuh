@@ -10,11 +10,17 @@
 //     through distributed shared memory and adds those of its own tokens in the order
 //     of the slices (deterministic, no workspace).
 //   - With W4_LAUNCH_PDL the first stages' weights are on their way while the previous
-//     kernel (the quantiser or the norm that makes x) still runs.
+//     kernel (the norm that makes x) still runs.
+//   - Up to 16 tokens are quantised here (T: the type of x): every CTA needs a slice of x
+//     small enough to encode while its weights arrive.  One token, 2560 x 9728 MXFP4: 6.0
+//     us, as two launches 6.6; nine tokens, 9728 x 2560 NVFP4 (two divisions per 16
+//     values, in every CTA): 8.8 us, as two launches 7.4, but the second launch costs the
+//     host 3.7 us.
 //
-// Warp roles (6 warps): 0 TMA producer; 1 tensor-memory allocation, scale copies and
-// MMAs; 2-5 epilogue (warp w reads lanes 32 (w % 4) .. + 31).  Every mbarrier wait is
-// bounded (fp4_mma.cuh).
+// Warp roles: 0 TMA producer; 1 tensor-memory allocation, scale copies and MMAs; 2-5
+// epilogue (warp w reads lanes 32 (w % 4) .. + 31); with x to quantise 2-7 do that
+// first (one token MXFP4 / nine NVFP4 as above: four warps 5.9 / 9.2 us, six 6.0 / 8.8,
+// twelve 6.6 / 8.7).  Every mbarrier wait is bounded (fp4_mma.cuh).
 #pragma once
 
 #include "fp4_mma.cuh"
@@ -25,10 +31,14 @@ namespace fgemm {
 
 namespace skinny {
 
-constexpr int kWarps = 6;
-constexpr int kThreads = kWarps * 32;
-constexpr int kEpiWarp0 = 2;
+constexpr int kEpiWarp0 = 2, kEpiWarps = 4;
 constexpr int kMaxSplit = 8;
+constexpr int kQuantWarps = 6;   // warps kEpiWarp0 on
+
+struct Quantised {};   // T of an x that is 4-bit already
+template <typename T> constexpr bool kFused = true;
+template <> constexpr bool kFused<Quantised> = false;
+template <typename T> constexpr int kThreads = 32 * (kEpiWarp0 + (kFused<T> ? kQuantWarps : kEpiWarps));
 
 template <int FMT, int NT>
 struct Config {
@@ -70,6 +80,10 @@ struct Params {
     int splits;                    // CTAs of a cluster: slices of K
     int out_type;
     int early_w;                   // the weights may be read before the previous kernel has completed
+    const void *x;                 // x to quantise: rows ldx values apart
+    long long ldx;
+    int ceil_rule;
+    int *d_status;
 };
 
 // The first `count` of n values of consecutive tokens, one column of y per lane.
@@ -112,8 +126,56 @@ __device__ __forceinline__ void add_slices(const Params &p, const Factor &fac, c
     }
 }
 
-template <int FMT, int NT>
-__global__ void __launch_bounds__(kThreads, 2) gemm_kernel(const __grid_constant__ CUtensorMap wmap,
+// Codes and scales of this CTA's tokens for the k of its stages, written where TMA would
+// have put them: rows of 128 bytes with the 128-byte swizzle, scale tiles; as many
+// stages at once as the ring holds.
+template <typename T, int FMT, int NT>
+__device__ __forceinline__ void quantize_stages(const Params &p, Shared<FMT, NT> &sh, int k0, int stages, int warp,
+                                                int lane, volatile int *abort, unsigned long long limit) {
+    constexpr int STAGES = Config<FMT, NT>::STAGES, WORDS = 8 * sizeof(T), NB = 32 / fp4::Format<FMT>::BLOCK;
+    const int zero = fp4::wait_prior_grid_zero();
+    const float g = FMT == W4_FMT_NVFP4 ? fp4::load_scalar(p.gx + zero) : 1.0f;
+    const T *x = reinterpret_cast<const T *>(p.x) + zero;
+    for (int b0 = 0; b0 < stages; b0 += STAGES) {
+        const int batch = min(STAGES, stages - b0), units = batch * p.M * 8;
+        if (b0 > 0) {
+            for (int s = 0; s < batch; s++) pipe_wait(&sh.empty[s], ((b0 / STAGES) - 1) & 1, abort, limit);
+            if (__any_sync(0xFFFFFFFFu, *abort != 0)) break;
+        }
+        for (int i0 = (warp - kEpiWarp0) * 32; i0 < units; i0 += kQuantWarps * 32) {
+            const int i = i0 + lane, u = lane & 7, s = (i >> 3) / p.M, row = (i >> 3) - s * p.M;
+            const int k = (k0 + b0 + s) * BK + u * 32;
+            uint32_t w[WORDS], c[4];
+            if (i < units && k < p.K) {
+                const uint32_t *src = reinterpret_cast<const uint32_t *>(x + (long long)row * p.ldx + k);
+#pragma unroll
+                for (int j = 0; j < WORDS; j += 4) fp4::load_words<4>(src + j, w + j);
+            } else {
+#pragma unroll
+                for (int j = 0; j < WORDS; j++) w[j] = 0u;
+            }
+            bool bad;
+            const uint32_t word = fp4::quantize32<T, FMT>(w, g, p.ceil_rule, c, bad);
+            if (i >= units) continue;
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
+                         ::"r"(smem_addr(sh.b[s]) + (uint32_t)(row * 128 + ((u ^ (row & 7)) * 16))),
+                         "r"(c[0]), "r"(c[1]), "r"(c[2]), "r"(c[3]) : "memory");
+            if (u * NB % 4 == 0)
+                asm volatile("st.shared.b32 [%0], %1;"
+                             ::"r"(smem_addr(sh.sfb[s][u * NB / 4]) + (uint32_t)(row * 16)), "r"(word) : "memory");
+            if (bad) fp4::report_nonfinite(p.d_status);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0)
+            for (int s = 0; s < batch; s++) mbar_arrive(&sh.full[s]);
+    }
+    __syncwarp();
+}
+
+// T: Quantised (x by TMA) or the type of an x of at most 16 tokens to quantise.
+template <int FMT, int NT, typename T>
+__global__ void __launch_bounds__(kThreads<T>, 2) gemm_kernel(const __grid_constant__ CUtensorMap wmap,
                                                          const __grid_constant__ CUtensorMap xmap,
                                                          const __grid_constant__ Params p) {
     using S = Shared<FMT, NT>;
@@ -134,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, 2) gemm_kernel(const __grid_constant
     if (threadIdx.x == 0) {
         sh.abort = 0;
         for (int i = 0; i < STAGES; i++) {
-            mbar_init(&sh.full[i], 1);
+            mbar_init(&sh.full[i], kFused<T> ? 1 + kQuantWarps : 1);
             mbar_init(&sh.empty[i], 1);
         }
         mbar_init(&sh.acc_full, 1);
@@ -159,7 +221,8 @@ __global__ void __launch_bounds__(kThreads, 2) gemm_kernel(const __grid_constant
         // scale tiles that exist in a stage (the last stage of a row may be cut)
         auto tiles = [&](int kt) { return min(C::ST, p.tiles_k - kt * C::ST); };
         auto load_w = [&](int kt, int s) {
-            mbar_arrive_expect_tx(&sh.full[s], A_BYTES + C::B_BYTES + 2 * (uint32_t)tiles(kt) * SF_TILE);
+            mbar_arrive_expect_tx(&sh.full[s], A_BYTES + (uint32_t)tiles(kt) * SF_TILE +
+                                                   (kFused<T> ? 0u : C::B_BYTES + (uint32_t)tiles(kt) * SF_TILE));
             tma_load_2d(sh.a[s], &wmap, kt * (BK / 2), n0, &sh.full[s]);
             bulk_load(sh.sfa[s], p.sfw + ((size_t)(n0 / 128) * p.tiles_k + kt * C::ST) * SF_TILE,
                       (uint32_t)tiles(kt) * SF_TILE, &sh.full[s]);
@@ -173,8 +236,9 @@ __global__ void __launch_bounds__(kThreads, 2) gemm_kernel(const __grid_constant
         for (int i = 0; i < first; i++)
             if (elect_one()) load_w(k0 + i, i);
         pdl_wait_prior_grid();   // x may be the previous kernel's output
-        for (int i = 0; i < first; i++)
-            if (elect_one()) load_x(k0 + i, i);
+        if (!kFused<T>)
+            for (int i = 0; i < first; i++)
+                if (elect_one()) load_x(k0 + i, i);
         int it = first;
         for (; it < k1 - k0; it++) {
             const int s = it % STAGES;
@@ -183,10 +247,13 @@ __global__ void __launch_bounds__(kThreads, 2) gemm_kernel(const __grid_constant
             if (__any_sync(0xFFFFFFFFu, *abort != 0)) break;
             if (elect_one()) {
                 load_w(k0 + it, s);
-                load_x(k0 + it, s);
+                if (!kFused<T>) load_x(k0 + it, s);
             }
         }
-        drain_ring(sh.full, STAGES, it);
+        // no load may land after the CTA has left (after an abort a stage may lack x that was
+        // not quantised: one full wait, and what was issued has landed)
+        for (int i = max(0, it - STAGES); i < it; i++)
+            if (!mbar_wait_bounded(&sh.full[i % STAGES], (uint32_t)((i / STAGES) & 1))) break;
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------- MMA issuer -------------------------------
@@ -225,13 +292,16 @@ __global__ void __launch_bounds__(kThreads, 2) gemm_kernel(const __grid_constant
         __syncwarp();
         mbar_wait_bounded(&sh.mma_done, 0);
         __syncwarp();
+    } else if constexpr (kFused<T>) {
+        quantize_stages<T, FMT, NT>(p, sh, k0, k1 - k0, warp, lane, abort, limit);
     }
 
     // -------------------------------- epilogue --------------------------------
     const int q = warp & 3, row = q * 32 + lane;            // row of w in the tile
     const int own = NT / p.splits;                          // tokens a CTA of the cluster adds up (a power of two)
     if (p.splits > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-    if (warp >= kEpiWarp0) {
+    const bool epilogue = warp >= kEpiWarp0 && warp < kEpiWarp0 + kEpiWarps;
+    if (epilogue) {
         pdl_wait_prior_grid();                              // y and the global scales belong to it until then
         // on expiry (abort) the accumulator is garbage, but the warp stays together
         pipe_wait(&sh.acc_full, 0, abort, limit);
@@ -265,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 2) gemm_kernel(const __grid_constant
     if (p.splits > 1) {
         // all partial sums are in place; after this no CTA touches another's shared memory
         asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-        if (warp >= kEpiWarp0 && n0 + row < p.N) {
+        if (epilogue && n0 + row < p.N) {
             const Factor fac(p.gw, p.gx);
             const int first = m0 + slice * own;
             if (own >= 8) add_slices<8>(p, fac, sh.red, own, first, n0, row);

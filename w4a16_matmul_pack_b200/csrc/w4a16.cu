@@ -726,6 +726,6 @@ w4_status w4_set_wait_limit(unsigned long long ns) {
     return fp4_set_wait_limit(v) == W4_OK ? W4_OK : W4_ERR_CUDA;
 }
 
-const char *w4_version(void) { return "w4a16 0.2.0 (sm_100a)"; }
+const char *w4_version(void) { return "w4a16 0.3.0 (sm_100a)"; }
 
 }  // extern "C"

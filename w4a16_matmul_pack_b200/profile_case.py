@@ -7,9 +7,15 @@
     python -m w4a16_matmul_pack_b200.profile_case q4_0 --K 9728 --N 9728
     python -m w4a16_matmul_pack_b200.profile_case recon --fmt nvfp4 --K 9728 --N 9728
     python -m w4a16_matmul_pack_b200.profile_case grouped --reps 3
+    python -m w4a16_matmul_pack_b200.profile_case w4a4 --fmt mxfp4 --M 2048 --K 2560 --N 9728
+    python -m w4a16_matmul_pack_b200.profile_case quantize --fmt mxfp4 --M 2048 --K 9728
+    python -m w4a16_matmul_pack_b200.profile_case norm --M 8192 --K 2560
 
 `grouped` runs the five decode-sweep matrices (K,N) = (2560,4096), (2560,1024),
 (4096,2560), (2560,9728), (9728,2560) at one token as one grouped launch.
+
+`w4a4`, `quantize` and `norm` run the W4A4 product (of operands quantised first),
+the activation quantiser and the block norms (post-norm, gate, residual, pre-norm).
 
 Inputs are the seeded synthetic matrices (Student-t weights, N(0,1) x; Laplace
 weights for ROCmFP4 and Q4_0).  Exits non-zero on any library or CUDA error.
@@ -32,8 +38,8 @@ import w4a16_matmul_pack_b200 as W4  # noqa: E402
 
 def main():
     ap = argparse.ArgumentParser()
-    ap.add_argument("op", choices=["gemv", "gemm", "pack", "grouped", "q4_0", "recon"])
-    ap.add_argument("--fmt", default="nvfp4", choices=["nvfp4", "dual", "fast"])
+    ap.add_argument("op", choices=["gemv", "gemm", "pack", "grouped", "q4_0", "recon", "w4a4", "quantize", "norm"])
+    ap.add_argument("--fmt", default="nvfp4", choices=["nvfp4", "dual", "fast", "mxfp4"])
     ap.add_argument("--M", type=int, default=1)
     ap.add_argument("--K", type=int, default=2560)
     ap.add_argument("--N", type=int, default=9728)
@@ -49,6 +55,22 @@ def main():
         torch.cuda.synchronize()
         for _ in range(a.reps):
             W4.w4a16_gemv_grouped(ws, xs, flags=a.flags)
+        finish()
+        return
+    if a.op in ("w4a4", "quantize", "norm"):
+        x = I.activations(a.M, a.K, 7, outlier_cols=16, device="cuda")
+        g = (x.float().abs().amax() / 2688.0).reshape(1)
+        if a.op == "norm":
+            ones = torch.ones(a.K, dtype=torch.bfloat16, device="cuda")
+            for _ in range(a.reps):
+                W4.block_norm(x, x, post_weight=ones, pre_weight=ones, gate=ones)
+        else:
+            q = W4.fp4_quantize(x, a.fmt, global_scale=g)
+            if a.op == "w4a4":
+                W = I.matrix("student_t4", a.N, a.K, 7, 0.02, 1e-4, 20.0, device="cuda")
+                w = W4.fp4_quantize(W, a.fmt, global_scale=g)
+            for _ in range(a.reps):
+                W4.w4a4_gemm(w, q) if a.op == "w4a4" else W4.fp4_quantize(x, a.fmt, global_scale=g, out=q)
         finish()
         return
     if a.fmt == "nvfp4" and a.op != "q4_0":
