@@ -339,7 +339,7 @@ typedef enum {
  * device memory, owned by the caller).
  *   fmt     W4_FMT_MXFP4: blocks of 32 values, scale = E8M0 byte b, 2^(b - 127)
  *           (0xFF: NaN).  W4_FMT_NVFP4: blocks of 16 values, scale = E4M3 byte
- *           (0x7F: NaN), times the global scale.
+ *           0x00..0x7E (no sign; 0x7F: NaN), times the global scale.
  *   codes   [rows][K/2] bytes, E2M1 nibbles as in w4_weights.
  *   scales  fp4_scale_bytes(fmt, rows, K) bytes: 4 consecutive scales of a row
  *           are one word; word j of row r is at byte
@@ -403,9 +403,9 @@ w4_status fp4_tile_scales(int fmt, int rows, int K, const uint8_t *row_scales, u
  *   w, x      operands of the same format and K.
  *   y         out, x->rows rows of w->rows values of out_type (w4_type), `ldy` >=
  *             w->rows values apart (any alignment of the rows; y on 16 bytes).
- *   flags     0, or W4_LAUNCH_PDL: the weights may be read while the previous
- *             kernel on the stream is still running (it must not write them); x
- *             is read and y written only after it has completed.
+ *   flags     0, or W4_LAUNCH_PDL: the weights may be read while earlier kernels
+ *             on the stream are still running (none of them may write the weights); x
+ *             is read and y written only after the previous one has completed.
  */
 w4_status w4a4_gemm(const w4_fp4 *w, const w4_fp4 *x, void *y, int out_type, long long ldy, unsigned flags,
                     void *stream);
@@ -428,7 +428,7 @@ typedef enum { W4_GATE_NONE = 0, W4_GATE_SIGMOID = 1, W4_GATE_TANH = 2 } w4_gate
 
 /*
  * w4_block_norm -- what stands between two blocks of a decoder, in one pass over
- * M rows of D values (1 <= D <= 32768, W4_ERR_UNSUPPORTED above):
+ * M rows of D values (1 <= D <= 32768, M <= 2^30, W4_ERR_UNSUPPORTED above):
  *   b  = y * rsqrt(mean(y^2) + eps) * (w_post + weight_offset)   (b = y without w_post)
  *   h' = residual_scale * h + block_scale * act(gate) * b        (no h: the second term alone)
  *   z  = h' * rsqrt(mean(h'^2) + eps) * (w_pre + weight_offset)  (no w_pre: factor 1)

@@ -121,7 +121,7 @@ def test_norm_refusals(lib):
     assert call(y=None) == ARG and call(z=None) == ARG and call(M=0) == ARG and call(D=0) == ARG
     assert call(type=4) == ARG and call(ldy=63) == ARG and call(ldz=10) == ARG
     assert call(eps=-1.0) == ARG and call(eps=float("nan")) == ARG
-    assert call(D=32769, ldy=40000, ldz=40000) == UNSUPPORTED
+    assert call(D=32769, ldy=40000, ldz=40000) == UNSUPPORTED and call(M=(1 << 30) + 1) == UNSUPPORTED
     assert call(h=16, ldh=3) == ARG and call(h_out=16, ldh_out=3) == ARG
     assert call(gate=16, ldgate=64, gate_rows=0) == ARG and call(gate=16, ldgate=10, gate_rows=1) == ARG
     assert call(gate_act=3) == ARG and call(gate_act=-1) == ARG

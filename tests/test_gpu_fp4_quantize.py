@@ -109,6 +109,16 @@ def test_zero_blocks_and_extremes(fmt):
         check(x, fmt, ceil=True)
 
 
+@pytest.mark.parametrize("g", [0.0, -1.0, float("inf")])
+def test_global_scales_that_leave_nothing(g):
+    """No value has a code under a global scale of zero, a negative or an infinite one:
+    all zeros."""
+    x = rows(3, 64, 2, torch.float32)
+    q = W4.fp4_quantize(x.cuda(), "nvfp4", global_scale=torch.tensor([g], device="cuda"))
+    scales, _ = R.untile(q.scales.cpu().numpy(), 3, 64, "nvfp4")
+    assert not scales.any() and not (q.codes & 0x77).any()
+
+
 @pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_nonfinite_blocks_are_nan(fmt, dtype):

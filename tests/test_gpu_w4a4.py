@@ -252,6 +252,29 @@ def test_captured_replayed_and_on_other_streams(fmt, M):
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+@pytest.mark.parametrize("M", [1, 16, 20, 300])
+def test_x_made_by_a_kernel_that_is_still_running(M):
+    """Every call waits for the kernel that makes its inputs (x, the global scale), however
+    long that takes, and the caller may overwrite x right behind it."""
+    N, K = 256, 1024
+    w, _ = operand(randn(N, K, seed=1, scale=0.02), "nvfp4")
+    xs = [randn(M, K, seed=5 + i).cuda() for i in range(2)]
+    gs = [scale_of(x) for x in xs]
+    want = [W4.w4a4_linear(w, x, global_scale=g) for x, g in zip(xs, gs)]
+    x, g = torch.empty_like(xs[0]), torch.empty(1, device="cuda")
+    big = torch.randn(4096, 4096, device="cuda")
+    for i in range(12):
+        (big @ big)                                # keeps the stream busy
+        x.copy_(xs[i % 2])
+        g.copy_(gs[i % 2])
+        y = W4.w4a4_linear(w, x, global_scale=g)
+        q = W4.fp4_quantize(x, "nvfp4", global_scale=g)
+        x.zero_(), g.zero_()                       # behind the calls
+        assert torch.equal(y, want[i % 2])
+        q2 = W4.fp4_quantize(xs[i % 2], "nvfp4", global_scale=gs[i % 2])
+        assert torch.equal(q.codes, q2.codes)
+
+
 def test_weights_read_before_the_previous_kernel_ends():
     """W4_LAUNCH_PDL behind the kernel that makes x: the same bits."""
     w, _ = operand(randn(2560, 2560, seed=1, scale=0.02), "mxfp4")

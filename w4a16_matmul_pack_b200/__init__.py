@@ -543,6 +543,8 @@ def fp4_quantize(x: torch.Tensor, fmt="mxfp4", *, global_scale: Optional[torch.T
 def fp4_dequantize(a: Fp4Tensor, dtype: torch.dtype = torch.bfloat16, *, out: Optional[torch.Tensor] = None,
                    stream=None) -> torch.Tensor:
     """The values [rows][K] an operand stands for (see fp4_dequantize in include/w4a16.h)."""
+    if not isinstance(a, Fp4Tensor):
+        raise ValueError("a must be an Fp4Tensor")
     if out is None:
         out = _new(a.rows, a.K, dtype, a.device)
     ptr, ld, _, _ = _rows(out, "out", a._dev, a.rows, a.K)

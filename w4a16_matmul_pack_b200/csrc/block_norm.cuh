@@ -25,7 +25,8 @@ namespace norm {
 
 enum { GATE_NONE = 0, GATE_SIGMOID = 1, GATE_TANH = 2 };
 
-constexpr int kMaxD = 32768;   // 1024 threads, four units each
+constexpr int kMaxD = 32768;      // 1024 threads, four units each
+constexpr int kMaxM = 1 << 30;    // a row and a grid's stride past the last fit an int
 
 // How a row's values are shared out.
 //   VECTOR    thread t, unit p: values 8 (p * threads + t) .. + 7, 16-byte accesses.

@@ -114,7 +114,7 @@ __device__ __forceinline__ uint32_t block_scale(uint32_t amax, float g, bool cei
         byte = g > 0.0f ? f32_to_e4m3(t) : (g != g ? 0x7Fu : 0u);
         f = __frcp_rn(__fmul_rn(e4m3_to_f32(byte), g));
         // s * g == 0, or too small for a binary32 reciprocal: a block of zeros
-        if (!(f <= 3.4028234e38f) && byte != 0x7Fu) byte = 0u, f = 0.0f;
+        if (!(fabsf(f) <= 3.4028234e38f) && byte != 0x7Fu) byte = 0u, f = 0.0f;
         if (amax >= 0x7F800000u || byte == 0x7Fu) byte = 0x7Fu, f = 0.0f;
     }
     return byte;

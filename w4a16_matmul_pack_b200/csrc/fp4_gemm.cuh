@@ -173,6 +173,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int n0 = tn * NT + (int)rank * (NT / 2);
             for (int kt = 0; kt < KT; kt++, it++) {
                 const int s = it % STAGES;
+                // (a wait's limit is not to run while the previous kernel does)
+                if (it == STAGES) pdl_wait_prior_grid();
                 if (it >= STAGES) pipe_wait(&sh.empty[s], ((it / STAGES) - 1) & 1, abort, limit);
                 // after an abort nothing more is loaded: the stage may not be free
                 stop = __any_sync(0xFFFFFFFFu, *abort != 0);
@@ -209,6 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 1) {
         // ------------------------------- MMA issuer -------------------------------
         if (rank == 0) {
+            pdl_wait_prior_grid();   // a wait's limit is not to run while the previous kernel does
             int it = 0, lt = 0;
             bool stop = false;
             const int steps = (p.K + 63) / 64;

@@ -257,6 +257,7 @@ __global__ void __launch_bounds__(kThreads<T>, 2) gemm_kernel(const __grid_const
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------- MMA issuer -------------------------------
+        pdl_wait_prior_grid();   // a wait's limit is not to run while the previous kernel does
         const int steps = (p.K + 63) / 64;
         const uint32_t sfa = tmem + C::ACC_COLS, sfb = sfa + 4 * C::ST;
         for (int it = 0; it < k1 - k0; it++) {

@@ -63,7 +63,7 @@ w4_status launch_norm_fmt(const norm::Args &a, int mode, int fmt, cudaStream_t s
 
 extern "C" w4_status w4_block_norm(const w4_norm *n, void *stream) {
     if (!n || !n->y || n->M < 1 || n->D < 1 || !is_type(n->type) || !(n->eps >= 0.0f)) return W4_ERR_ARG;
-    if (n->D > norm::kMaxD) return W4_ERR_UNSUPPORTED;
+    if (n->D > norm::kMaxD || n->M > norm::kMaxM) return W4_ERR_UNSUPPORTED;
     if (n->ldy < n->D || (n->h && n->ldh < n->D) || (n->h_out && n->ldh_out < n->D)) return W4_ERR_ARG;
     if (n->gate && (n->gate_rows < 1 || n->ldgate < n->D)) return W4_ERR_ARG;
     if (n->gate_act < W4_GATE_NONE || n->gate_act > W4_GATE_TANH) return W4_ERR_ARG;
