@@ -400,14 +400,17 @@ def _new(rows: int, width: int, dtype, device) -> torch.Tensor:
 def _rows(t: torch.Tensor, name: str, dev=None, rows=None, width=None):
     """(data pointer, row distance, rows, width) of a 2-D CUDA tensor with contiguous
     rows, on device `dev` and of the given shape where these are given."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    try:
+        d = t.get_device()
+        (r, w), (s0, s1) = t.shape, t.stride()
+    except (AttributeError, TypeError, ValueError):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor (no CPU path)") from None
+        raise ValueError(f"{name} must have two dimensions, got {tuple(t.shape)}") from None
+    if d < 0:
         raise ValueError(f"{name} must be a CUDA tensor (no CPU path)")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must have two dimensions, got {tuple(t.shape)}")
-    r, w = t.shape
-    if (rows is not None and (r != rows or w != width)) or (dev is not None and t.get_device() != dev):
+    if (rows is not None and (r != rows or w != width)) or (dev is not None and d != dev):
         raise ValueError(f"{name} must have shape {(rows, width)} on cuda:{dev}, got {(r, w)} on {t.device}")
-    s0, s1 = t.stride()
     if s1 != 1 and w > 1:
         raise ValueError(f"{name} must have contiguous rows")
     return t.data_ptr(), s0 if r > 1 else w, r, w
@@ -417,8 +420,9 @@ def _vector(t: Optional[torch.Tensor], name: str, dtype, dev: int, n: int) -> in
     """Data pointer of an optional contiguous tensor of n values on device dev (0: none)."""
     if t is None:
         return 0
-    _cuda(t, name, dtype)
-    if t.numel() != n or t.get_device() != dev:
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.get_device() != dev or t.numel() != n \
+            or not t.is_contiguous():
+        _cuda(t, name, dtype)
         raise ValueError(f"{name} must hold {n} values on cuda:{dev}, got {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
