@@ -83,6 +83,19 @@ def test_output_types_and_row_distance(fmt, M, dtype, N):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("M,N,K", [
+    (513, 1001, 2592), (300, 9728, 256), (1300, 3333, 800), (2304, 4104, 160), (700, 6100, 608), (1025, 9700, 288),
+    (2100, 3999, 320)])
+def test_wide_tiles(fmt, dtype, M, N, K):
+    """Prompts whose tiles are 128, 192 (the next three) and 256 rows of w (the last
+    three) on 148 SMs, one to several tiles per CTA pair; rows of y on and off 16 bytes."""
+    x, xv = operand(randn(M, K, seed=M + K), fmt)
+    w, wv = operand(randn(N, K, seed=N + K + 1, scale=0.02), fmt)
+    check(W4.w4a4_gemm(w, x, out_dtype=dtype), xv, wv, dtype)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("M,K,N", [(1, 2560, 9728), (9, 9728, 2560), (16, 4096, 2560), (48, 2560, 1024), (2048, 2560, 1024)])
 def test_layer_shapes(fmt, M, K, N):
     """The projections' shapes, weights with outliers; sampled rows of w, every token."""

@@ -284,21 +284,24 @@ w4_status fused_linear(const w4_fp4 *w, const PlainX &x, void *y, long long ldy,
     }
 }
 
-// Width of a prompt's tiles: the least of launch + waves x (stages x time per stage +
-// time per tile), in us as measured on 148 SMs.  A stage is bound by its loads (0.31
-// us for 256 tokens x 256 rows, 0.255 for 192, 0.24 for 128); tiles of 256 rows share
-// tensor memory between two accumulators and wait for it (1.8 us a tile).  2048 x 2560 x
-// 9728: 23.6 us at 192, 27.5 at 256, 29.6 at 128; 8192 x 9728 x 2560: 73.9 at 256, 77.8
-// at 192.
+// Width of a prompt's tiles: the least of launch + waves x max(stages x time per stage
+// + time per tile, time to store a tile), in us: a least-squares fit to 22 shapes of
+// 200 .. 8192 tokens, K 32 .. 30000, N 96 .. 9728 on 148 SMs (its choice is within 0.3%
+// of the best on average, 14 shapes that were not fitted among them).  A stage is bound by its
+// loads; tiles of 256 rows share tensor memory between two accumulators and wait for it
+// (1.8 us a tile); short K is bound by the stores.  Measured at 128 / 192 / 256 rows
+// (MXFP4): 2048 x 2560 x 9728 28.0 / 22.9 / 27.6 us; 8192 x 9728 x 2560 82.1 / 71.9 /
+// 71.8; 512 x 2560 x 2560 7.2 / 8.0 / 9.0; 8192 x 256 x 1024 10.2 / 10.1 / 8.8.
 int tile_width(int M, int N, int K, int sms) {
-    const struct { int nt; double launch, stage, tile; } kinds[] = {
-        {128, 5.2, 0.24, 0.3}, {192, 5.6, 0.255, 0.4}, {256, 5.9, 0.31, 1.8}};
+    const struct { int nt; double launch, stage, tile, store; } kinds[] = {
+        {128, 4.33, 0.214, 0.59, 1.51}, {192, 4.49, 0.243, 0.86, 1.96}, {256, 3.95, 0.314, 1.80, 2.29}};
     const long long pairs = std::max(1, sms / 2), stages = (K + fgemm::BK - 1) / fgemm::BK;
     int best = 0;
     double least = 0;
     for (const auto &k : kinds) {
         const long long tiles = (long long)((M + 255) / 256) * ((N + k.nt - 1) / k.nt);
-        const double t = k.launch + (double)((tiles + pairs - 1) / pairs) * (stages * k.stage + k.tile);
+        const long long waves = (tiles + pairs - 1) / pairs;
+        const double t = k.launch + (double)waves * std::max((double)stages * k.stage + k.tile, k.store);
         if (!best || t < least) best = k.nt, least = t;
     }
     return best;
