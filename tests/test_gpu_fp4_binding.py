@@ -70,3 +70,42 @@ def test_block_norm():
     refused(lambda: W4.block_norm(x(1, 64).expand(4, 64)), W4.W4Error)
     refused(lambda: W4.block_norm(x(1, 32800)), W4.W4Error)
     refused(lambda: W4.block_norm(y, eps=-1.0), W4.W4Error)
+
+
+def test_memory_of_a_call_on_another_stream():
+    """What a call allocates belongs to the stream it runs on: a workspace given back
+    while that stream is busy is not handed to the current stream, and a result does not
+    take memory that the current stream still reads."""
+    torch.manual_seed(0)
+    w = W4.fp4_quantize(torch.randn(256, 1024, device="cuda").bfloat16())
+    a = torch.randn(300, 1024, device="cuda").bfloat16()
+    want = W4.w4a4_linear(w, a)
+    need = W4.w4a4_workspace_bytes(w, 300)
+    big = torch.randn(4096, 4096, device="cuda")
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        with torch.cuda.stream(st):
+            big @ big                                  # keeps the stream busy
+        y = W4.w4a4_linear(w, a, stream=st)
+        others = [torch.full((need,), 255, dtype=torch.uint8, device="cuda") for _ in range(4)]
+        torch.cuda.synchronize()
+        assert torch.equal(y, want)
+        del others
+    src = torch.full((300, 256), 7.0, dtype=torch.bfloat16, device="cuda")
+    dst = torch.zeros_like(src)
+    torch.cuda.synchronize()
+    big @ big
+    dst.copy_(src)                                     # behind the product, on the current stream
+    del src
+    ys = [W4.w4a4_linear(w, a, stream=st) for _ in range(4)]
+    torch.cuda.synchronize()
+    assert (dst == 7).all() and all(torch.equal(y, want) for y in ys)
+    with torch.cuda.stream(st):
+        z = W4.block_norm(a, quantize="mxfp4")[1]
+    st.synchronize()
+    for f in (lambda: W4.fp4_quantize(a, stream=st), lambda: W4.block_norm(a, quantize="mxfp4", stream=st)[1]):
+        q = f()
+        st.synchronize()
+        assert q.codes.shape == z.codes.shape and q.scales.numel() == z.scales.numel()
+        assert q._buf.data_ptr() % 512 == 0

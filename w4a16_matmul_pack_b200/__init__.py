@@ -392,8 +392,13 @@ def _type(t: torch.Tensor, name: str) -> int:
     return v
 
 
-def _new(rows: int, width: int, dtype, device) -> torch.Tensor:
-    """torch.empty((rows, width)), by the call that costs the host least."""
+def _new(rows: int, width: int, dtype, device, stream=None) -> torch.Tensor:
+    """torch.empty((rows, width)), by the call that costs the host least.  It belongs to the
+    stream the call runs on, as if the caller had made that stream the current one: what the
+    current stream still reads is not handed out, nor is what this stream still writes."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return _new(rows, width, dtype, device)
     return torch.empty_strided((rows, width), (width, 1), dtype=dtype, device=device)
 
 
@@ -479,14 +484,14 @@ class Fp4Tensor:
         self._c = _pack_fp4(fmt, rows, K, self._codes_ptr, self._scales_ptr, self._gptr)
 
     @classmethod
-    def _empty(cls, fmt: int, rows: int, K: int, device: torch.device, dev: int, global_scale, gptr: int):
+    def _empty(cls, fmt: int, rows: int, K: int, device: torch.device, dev: int, global_scale, gptr: int, stream):
         """A new operand whose codes and scales are two parts of one allocation."""
         n = fp4_scale_bytes(fmt, rows, K)
         if not n:
             raise W4Error(1, f"4-bit operand of {rows} x {K} (K % 32 == 0, one row at least)")
         at = (rows * (K // 2) + 255) & ~255
         self = cls.__new__(cls)
-        self._buf = torch.empty_strided((at + n,), (1,), dtype=torch.uint8, device=device)
+        self._buf = _new(1, at + n, torch.uint8, device, stream)
         p = self._buf.data_ptr()
         self.fmt, self.rows, self.K, self.global_scale = fmt, rows, K, global_scale
         self._codes = self._scales = None
@@ -498,13 +503,13 @@ class Fp4Tensor:
     @property
     def codes(self) -> torch.Tensor:
         if self._codes is None:
-            self._codes = self._buf[:self.rows * (self.K // 2)].view(self.rows, self.K // 2)
+            self._codes = self._buf[0, :self.rows * (self.K // 2)].view(self.rows, self.K // 2)
         return self._codes
 
     @property
     def scales(self) -> torch.Tensor:
         if self._scales is None:
-            self._scales = self._buf[self._scales_at:]
+            self._scales = self._buf[0, self._scales_at:]
         return self._scales
 
     @property
@@ -516,13 +521,14 @@ class Fp4Tensor:
         return f"Fp4Tensor({name}, rows={self.rows}, K={self.K}, device={self.device})"
 
 
-def _result(out: Optional[Fp4Tensor], fmt: int, rows: int, K: int, device, dev: int, global_scale) -> Fp4Tensor:
+def _result(out: Optional[Fp4Tensor], fmt: int, rows: int, K: int, device, dev: int, global_scale,
+            stream) -> Fp4Tensor:
     """The operand a quantiser writes: `out`, checked, or a new one."""
     g = _vector(global_scale, "global_scale", torch.float32, dev, 1) if fmt == FMT_NVFP4 else 0
     if out is None:
         if fmt == FMT_NVFP4 and not g:
             raise ValueError("nvfp4 needs a global_scale")
-        return Fp4Tensor._empty(fmt, rows, K, device, dev, global_scale if g else None, g)
+        return Fp4Tensor._empty(fmt, rows, K, device, dev, global_scale if g else None, g, stream)
     if not isinstance(out, Fp4Tensor) or (out.fmt, out.rows, out.K, out._dev) != (fmt, rows, K, dev):
         raise ValueError("out must be an Fp4Tensor of the result's format, shape and device")
     if g and g != out._gptr:
@@ -538,7 +544,7 @@ def fp4_quantize(x: torch.Tensor, fmt="mxfp4", *, global_scale: Optional[torch.T
     fmt = _fp4_fmt(fmt)
     ptr, ld, rows, K = _rows(x, "x")
     dev = x.get_device()
-    out = _result(out, fmt, rows, K, x.device, dev, global_scale)
+    out = _result(out, fmt, rows, K, x.device, dev, global_scale, stream)
     _call(dev, stream, "fp4_quantize", lib().fp4_quantize, ptr, _type(x, "x"), ld, rows, K, fmt, scale_rule, out._gptr,
           out._codes_ptr, out._scales_ptr, _vector(d_status, "d_status", torch.int32, dev, 1))
     return out
@@ -550,7 +556,7 @@ def fp4_dequantize(a: Fp4Tensor, dtype: torch.dtype = torch.bfloat16, *, out: Op
     if not isinstance(a, Fp4Tensor):
         raise ValueError("a must be an Fp4Tensor")
     if out is None:
-        out = _new(a.rows, a.K, dtype, a.device)
+        out = _new(a.rows, a.K, dtype, a.device, stream)
     ptr, ld, _, _ = _rows(out, "out", a._dev, a.rows, a.K)
     _call(a._dev, stream, "fp4_dequantize", lib().fp4_dequantize, a._c, ptr, _type(out, "out"), ld)
     return out
@@ -566,8 +572,8 @@ def fp4_from_rows(fmt, codes: torch.Tensor, row_scales: torch.Tensor, global_sca
         raise ValueError("codes must have shape [rows][K/2]")
     rows, K, dev = codes.shape[0], 2 * codes.shape[1], codes.get_device()
     src = _vector(row_scales, "row_scales", torch.uint8, dev, rows * (K // (32 if fmt == FMT_MXFP4 else 16)))
-    out = Fp4Tensor(fmt, rows, K, codes,
-                    torch.empty(fp4_scale_bytes(fmt, rows, K), dtype=torch.uint8, device=codes.device), global_scale)
+    scales = _new(1, fp4_scale_bytes(fmt, rows, K), torch.uint8, codes.device, stream)[0]
+    out = Fp4Tensor(fmt, rows, K, codes, scales, global_scale)
     _call(dev, stream, "fp4_tile_scales", lib().fp4_tile_scales, fmt, rows, K, src, out._scales_ptr)
     return out
 
@@ -590,7 +596,7 @@ def w4a4_gemm(w: Fp4Tensor, x: Fp4Tensor, *, out_dtype: torch.dtype = torch.bflo
     if w._dev != dev:
         raise ValueError(f"w must be on cuda:{dev}, got cuda:{w._dev}")
     if out is None:
-        out = _new(x.rows, w.rows, out_dtype, x.device)
+        out = _new(x.rows, w.rows, out_dtype, x.device, stream)
     ptr, ld, _, _ = _rows(out, "out", dev, x.rows, w.rows)
     _call(dev, stream, "w4a4_gemm", lib().w4a4_gemm, w._c, x._c, ptr, _type(out, "out"), ld, flags)
     return out
@@ -616,7 +622,7 @@ def w4a4_linear(w: Fp4Tensor, x: torch.Tensor, *, global_scale: Optional[torch.T
     g = _vector(global_scale, "global_scale", torch.float32, dev, 1) if w.fmt == FMT_NVFP4 else 0
     device = x.device
     if out is None:
-        out = _new(M, w.rows, out_dtype, device)
+        out = _new(M, w.rows, out_dtype, device, stream)
     yptr, yld, _, _ = _rows(out, "out", dev, M, w.rows)
     wptr = need = 0
     if workspace is not None:
@@ -626,7 +632,7 @@ def w4a4_linear(w: Fp4Tensor, x: torch.Tensor, *, global_scale: Optional[torch.T
             raise ValueError(f"workspace must be on cuda:{dev}, got {workspace.device}")
     elif M > _FUSED_TOKENS:
         need = w4a4_workspace_bytes(w, M)
-        workspace = torch.empty_strided((need,), (1,), dtype=torch.uint8, device=device)
+        workspace = _new(1, need, torch.uint8, device, stream)
         wptr = workspace.data_ptr()
     _call(dev, stream, "w4a4_linear", lib().w4a4_linear, w._c, ptr, _type(x, "x"), ld, M, scale_rule, g, yptr,
           _type(out, "out"), yld, wptr, need, _vector(d_status, "d_status", torch.int32, dev, 1))
@@ -682,18 +688,18 @@ def block_norm(y: torch.Tensor, h: Optional[torch.Tensor] = None, *, post_weight
     if out_h is not None:
         ohp, ldoh, _, _ = rows_of(out_h, "out_h")
     elif want_h:
-        out_h = _new(M, D, dt, device)
+        out_h = _new(M, D, dt, device, stream)
         ohp, ldoh = out_h.data_ptr(), D
     fmt = qg = qc = qs = qd = 0
     if quantize is None:
         if out is None:
-            out = _new(M, D, dt, device)
+            out = _new(M, D, dt, device, stream)
             zp, ldz = out.data_ptr(), D
         else:
             zp, ldz, _, _ = rows_of(out, "out")
     else:
         fmt = _fp4_fmt(quantize)
-        out = _result(out, fmt, M, D, device, dev, global_scale)
+        out = _result(out, fmt, M, D, device, dev, global_scale, stream)
         qg, qc, qs = out._gptr, out._codes_ptr, out._scales_ptr
         qd = _vector(d_status, "d_status", torch.int32, dev, 1)
     n = _pack_norm(t, M, D, yp, hp, _vector(post_weight, "post_weight", dt, dev, D),
