@@ -139,6 +139,7 @@ w4_status launch_skinny(const w4_fp4 *w, const w4_fp4 *x, const PlainX &plain, v
     p.ldx = plain.ldx;
     p.ceil_rule = plain.ceil_rule;
     p.d_status = plain.d_status;
+    p.inv_m = M > 1 ? 0xFFFFFFFFu / (unsigned)M + 1u : 0u;
     p.splits = splits;
     p.out_type = out_type;
     p.early_w = early_w;

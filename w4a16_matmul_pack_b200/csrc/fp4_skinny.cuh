@@ -14,13 +14,13 @@
 //   - Up to 16 tokens are quantised here (T: the type of x): every CTA needs a slice of x
 //     small enough to encode while its weights arrive.  One token, 2560 x 9728 MXFP4: 6.0
 //     us, as two launches 6.6; nine tokens, 9728 x 2560 NVFP4 (two divisions per 16
-//     values, in every CTA): 8.8 us, as two launches 7.4, but the second launch costs the
+//     values, in every CTA): 8.6 us, as two launches 7.4, but the second launch costs the
 //     host 3.7 us.
 //
 // Warp roles: 0 TMA producer; 1 tensor-memory allocation, scale copies and MMAs; 2-5
 // epilogue (warp w reads lanes 32 (w % 4) .. + 31); with x to quantise 2-7 do that
 // first (one token MXFP4 / nine NVFP4 as above: four warps 5.9 / 9.2 us, six 6.0 / 8.8,
-// twelve 6.6 / 8.7).  Every mbarrier wait is bounded (fp4_mma.cuh).
+// twelve 6.6 / 8.7, before the last steps).  Every mbarrier wait is bounded (fp4_mma.cuh).
 #pragma once
 
 #include "fp4_mma.cuh"
@@ -84,6 +84,7 @@ struct Params {
     long long ldx;
     int ceil_rule;
     int *d_status;
+    uint32_t inv_m;                // ceil(2^32 / M) (M > 1): (i * inv_m) >> 32 = i / M below 2^28
 };
 
 // The first `count` of n values of consecutive tokens, one column of y per lane.
@@ -143,7 +144,9 @@ __device__ __forceinline__ void quantize_stages(const Params &p, Shared<FMT, NT>
             if (__any_sync(0xFFFFFFFFu, *abort != 0)) break;
         }
         for (int i0 = (warp - kEpiWarp0) * 32; i0 < units; i0 += kQuantWarps * 32) {
-            const int i = i0 + lane, u = lane & 7, s = (i >> 3) / p.M, row = (i >> 3) - s * p.M;
+            // (a division by M here costs 0.1 to 0.3 us of a call)
+            const int i = i0 + lane, u = lane & 7, j = i >> 3;
+            const int s = p.M == 1 ? j : (int)__umulhi((uint32_t)j, p.inv_m), row = j - s * p.M;
             const int k = (k0 + b0 + s) * BK + u * 32;
             uint32_t w[WORDS], c[4];
             if (i < units && k < p.K) {
