@@ -54,3 +54,29 @@ def test_nonfinite_inputs_reach_the_sticky_word_from_every_kernel():
         assert W4.w4_device_error(clear=False) == 5
         assert W4.w4_device_error(clear=True) == 5
         assert W4.w4_device_error(clear=True) == 0
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("M,N,K", [(8192, 2560, 9728), (2048, 9728, 2560), (300, 9728, 30016)])
+def test_a_pair_that_gives_up_frees_no_more_stages(fmt, M, N, K):
+    """Up to 190 stages per pair of CTAs, waits expired from the first one on.  The pair's
+    MMA issuer stops with its waiter: stages freed after the first CTA has stopped arming
+    its barriers would have the second CTA's loads counted on them, past what they hold.
+    Three times over, then right results on the same memory."""
+    g = torch.tensor([0.002], device="cuda") if fmt == "nvfp4" else None
+    gen = torch.Generator(device="cuda").manual_seed(K)
+    x = W4.fp4_quantize(torch.randn(M, K, generator=gen, device="cuda").bfloat16(), fmt, global_scale=g)
+    w = W4.fp4_quantize(torch.randn(N, K, generator=gen, device="cuda").bfloat16(), fmt, global_scale=g)
+    want = W4.w4a4_gemm(w, x)
+    out = torch.empty_like(want)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        W4.set_wait_limit(1)
+        t = time.monotonic()
+        W4.w4a4_gemm(w, x, out=out)
+        torch.cuda.synchronize()
+        assert time.monotonic() - t < 30
+        assert W4.w4_device_error(clear=True) == W4_ERR_TIMEOUT
+        W4.set_wait_limit(0)
+        assert torch.equal(W4.w4a4_gemm(w, x, out=out), want)
+        assert W4.w4_device_error(clear=True) == 0

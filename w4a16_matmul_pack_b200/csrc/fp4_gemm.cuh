@@ -118,6 +118,13 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
 
+// This word in the other CTA of the pair.
+__device__ __forceinline__ void store_in_other_cta(volatile int *p, int v, uint32_t rank) {
+    asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\t"
+                 "st.shared::cluster.b32 [a], %2;\n\t}"
+                 ::"r"(smem_addr(const_cast<int *>(p))), "r"(rank ^ 1u), "r"(v) : "memory");
+}
+
 // TMA: y leaves as TMA boxes (its rows start and end on 16 bytes).
 template <int FMT, int NT, bool TMA>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -202,9 +209,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // and both meet in the cluster barrier at the end
         if (rank == 0 && is_w) {
             // (after an abort a stage may lack the loads the other CTA or warp did not issue:
-            // one full wait, and what was issued has landed)
-            for (int i = max(0, it - STAGES); i < it; i++)
-                if (!mbar_wait_bounded(&sh.full[i % STAGES], (uint32_t)((i / STAGES) & 1))) break;
+            // settle() at the end takes this wait's place)
+            for (int i = max(0, it - STAGES); i < it && !*abort; i++)
+                if (!mbar_wait_bounded(&sh.full[i % STAGES], (uint32_t)((i / STAGES) & 1))) *abort = 1;
         }
         for (int i = max(0, it - STAGES); i < it; i++)
             pipe_wait(&sh.empty[i % STAGES], (i / STAGES) & 1, abort, limit);
@@ -214,7 +221,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Warp kWaitWarp does its mbarrier waits and meets it at named barrier 1 once per
         // stage (an accumulator's wait comes before its tile's first stage): with one warp
         // that waits and issues, 2048 x 9728 x 2560 took 25.1 / 27.0 us (MXFP4 / NVFP4),
-        // so 23.2 / 24.1.  After an abort it issues on stages that hold anything.
+        // so 23.2 / 24.1.
+        //
+        // After an abort it issues on stages that hold anything, but frees none: the abort
+        // flag is one CTA's, and freed stages would have the second CTA go on loading, with
+        // bytes counted on barriers that the first no longer arms.  A barrier holds less than
+        // 2^20 such bytes (27 fills of an NVFP4 stage of 256 rows); as it is, a stage is
+        // filled at most once more: 2 STAGE_BYTES.  (The flag is read ahead of the issue and
+        // used behind it: 512 x 2560 x 9728 MXFP4 10.8 -> 10.9 us, longer products as before;
+        // a barrier that also reduces a flag of the waiter 11.0.)
         if (rank == 0) {
             int it = 0, lt = 0;
             const int steps = (p.K + 63) / 64;
@@ -225,6 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int kt = 0; kt < KT; kt++, it++) {
                     const int s = it % STAGES;
                     named_barrier_sync(1, 64);
+                    const bool aborted = *abort != 0;   // set before the waiter's wait returned, if that expired
                     tc_fence_after();
                     if (elect_one()) {
                         const uint32_t a = codes_desc(smem_addr(sh.a[s])), b = codes_desc(smem_addr(sh.b[s]));
@@ -243,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 mma_fp4<FMT, 2>(acc, a + 2 * j, b + 2 * j, idesc<FMT>(2 * BM, NT) | scale_ids<FMT>(j),
                                                 sfa + 4 * c, sfb + 4 * c * C::GB + shift, (kt | j) ? 1u : 0u);
                         }
-                        commit_pair(&sh.empty[s]);
+                        if (!aborted) commit_pair(&sh.empty[s]);
                         if (kt == KT - 1) commit_pair(&sh.acc_full[lt & 1]);
                     }
                     __syncwarp();
@@ -255,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];"
                              ::"r"(smem_addr(&sh.mma_done)) : "memory");
             __syncwarp();
-            mbar_wait_bounded(&sh.mma_done, 0);
+            if (!mbar_wait_bounded(&sh.mma_done, 0)) *abort = 1;
         }
         __syncwarp();
     } else if (warp == kWaitWarp) {
@@ -315,7 +331,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     tc_fence_before();
     __syncthreads();
+    // After an abort in either CTA no barrier tells when the loads into both, which count on
+    // the first's barriers, and the arrivals of commits have landed: neither leaves before
+    // they must have.
+    if (threadIdx.x == 0 && *abort) store_in_other_cta(abort, 1, rank);
+    __syncwarp();
     cluster_sync();
+    if (*abort) {
+        if (threadIdx.x == 0) settle();
+        __syncthreads();
+        cluster_sync();
+    }
     if (warp == 1) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));

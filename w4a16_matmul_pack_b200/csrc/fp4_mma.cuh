@@ -130,6 +130,12 @@ __device__ __forceinline__ bool pipe_wait(uint64_t *bar, uint32_t parity, volati
     return mbar_wait(bar, parity, abort);
 }
 
+// As long as a bounded wait (2 s): what is in flight when it begins has landed.
+__device__ __forceinline__ void settle() {
+    const unsigned long long t0 = global_ns();
+    for (int i = 0; i < (1 << 26) && global_ns() - t0 < kWaitLimitNs; i++) __nanosleep(1000);
+}
+
 // gx * gw: one binary32 factor when it is a normal number or zero, else applied
 // in binary64 per value (the factor may leave binary32's range when the result
 // does not).
