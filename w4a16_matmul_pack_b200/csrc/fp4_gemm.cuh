@@ -204,6 +204,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         }
+        // (work of no more stages than the ring holds comes here without having waited)
+        pdl_wait_prior_grid();
         // no load may land and no commit arrive after this CTA has left: the first CTA
         // waits for both CTAs' loads, each for the MMAs' arrivals on its own barriers,
         // and both meet in the cluster barrier at the end
