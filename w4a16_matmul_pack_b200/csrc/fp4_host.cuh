@@ -86,8 +86,9 @@ inline w4_status launch_behind(void (*kernel)(P...), unsigned grid, unsigned thr
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...) == cudaSuccess ? launch_status() : W4_ERR_CUDA;
 }
 
-// This translation unit's sticky error word: added to *out if that is 0.
-inline w4_status take_device_error(int *out, int clear) {
+// This translation unit's sticky error word (each unit has its own, so the function is each
+// unit's own too): added to *out if that is 0.
+static inline w4_status take_device_error(int *out, int clear) {
     int v = 0;
     const int zero = 0;
     if (cudaMemcpyFromSymbol(&v, g_device_error, sizeof(int)) != cudaSuccess) return W4_ERR_CUDA;
