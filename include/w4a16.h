@@ -336,7 +336,8 @@ typedef enum {
 /*
  * A block-scaled 4-bit operand of the W4A4 product: `rows` rows (tokens, or the
  * output features of a weight matrix) of K values, K % 32 == 0 (all pointers
- * device memory, owned by the caller).
+ * device memory, owned by the caller); rows and K at most 2^31 - 256
+ * (W4_ERR_UNSUPPORTED above).
  *   fmt     W4_FMT_MXFP4: blocks of 32 values, scale = E8M0 byte b, 2^(b - 127)
  *           (0xFF: NaN).  W4_FMT_NVFP4: blocks of 16 values, scale = E4M3 byte
  *           0x00..0x7E (no sign; 0x7F: NaN), times the global scale.

@@ -140,3 +140,23 @@ def test_binding_refuses_cpu_tensors():
             f()
     with pytest.raises(ValueError):
         W4.fp4_quantize(x, "dual")
+
+
+def test_largest_extents(lib):
+    """Rows and K whose last tile would pass an int are refused, not wrapped."""
+    top = 2 ** 31 - 256
+    for fmt, per in ((W4.FMT_MXFP4, 128), (W4.FMT_NVFP4, 64)):
+        for rows, K in ((top, 32), (1, top)):
+            want = -(-rows // 128) * -(-K // per) * 512
+            assert lib.fp4_scale_bytes(fmt, rows, K) == W4.fp4_scale_bytes(fmt, rows, K) == want
+        for rows, K in ((top + 1, 32), (2 ** 31 - 1, 32), (1, 2 ** 31 - 32), (130, 2 ** 31 - 96)):
+            assert lib.fp4_scale_bytes(fmt, rows, K) == W4.fp4_scale_bytes(fmt, rows, K) == 0
+            g = 16 if fmt == W4.FMT_NVFP4 else None
+            big, w = operand(fmt, rows, K, g=g), operand(fmt, 8, K, g=g)
+            assert lib.fp4_quantize(P(16), 0, K, rows, K, fmt, 0, g, P(16), P(16), None, None) == UNSUPPORTED
+            assert lib.fp4_dequantize(ctypes.byref(big), P(16), 0, K, None) == UNSUPPORTED
+            assert lib.fp4_tile_scales(fmt, rows, K, P(16), P(16), None) == UNSUPPORTED
+            assert lib.w4a4_gemm(ctypes.byref(big), ctypes.byref(w), P(16), 0, rows, 0, None) == UNSUPPORTED
+            assert lib.w4a4_gemm(ctypes.byref(w), ctypes.byref(big), P(16), 0, 8, 0, None) == UNSUPPORTED
+            assert lib.w4a4_linear(ctypes.byref(w), P(16), 0, K, rows, 0, g, P(16), 0, 8, P(256), 1 << 60, None,
+                                   None) == UNSUPPORTED

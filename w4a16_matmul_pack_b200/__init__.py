@@ -371,6 +371,7 @@ def w4a16_gemm(w: PackedWeights, x: torch.Tensor, *, want_f32: bool = True, want
 _TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _FP4_FMTS = {"mxfp4": FMT_MXFP4, "nvfp4": FMT_NVFP4, FMT_MXFP4: FMT_MXFP4, FMT_NVFP4: FMT_NVFP4}
 _GATES = {"none": 0, "sigmoid": 1, "tanh": 2}
+_MAX_EXTENT = 2 ** 31 - 256   # rows and K of an operand
 _FUSED_TOKENS = 16   # tokens up to which w4a4_linear needs no workspace
 _pack_fp4 = struct.Struct("@iiiPPP").pack                              # w4_fp4
 _pack_norm = struct.Struct("@iiiPPPPPqqqiiffffPqPqiiPPPP").pack        # w4_norm
@@ -448,7 +449,7 @@ def _call(dev: int, stream, what: str, fn, *args):
 
 def fp4_scale_bytes(fmt: int, rows: int, K: int) -> int:
     """Bytes of an operand's scale tiles (as fp4_scale_bytes in include/w4a16.h)."""
-    if fmt not in (FMT_MXFP4, FMT_NVFP4) or rows < 1 or K < 32 or K % 32:
+    if fmt not in (FMT_MXFP4, FMT_NVFP4) or rows < 1 or K < 32 or K % 32 or max(rows, K) > _MAX_EXTENT:
         return 0
     return (rows + 127) // 128 * ((K + 127) // 128 if fmt == FMT_MXFP4 else (K + 63) // 64) * 512
 

@@ -352,7 +352,7 @@ size_t linear_scales_at(int rows, int K) { return ((size_t)rows * (K / 2) + 255)
 extern "C" {
 
 size_t fp4_scale_bytes(int fmt, int rows, int K) {
-    if (!is_fp4(fmt) || rows < 1 || K < 32 || K % 32) return 0;
+    if (!is_fp4(fmt) || rows < 1 || K < 32 || K % 32 || too_large(rows, K)) return 0;
     return ((size_t)rows + 127) / 128 * fp4::scale_tiles_k(fmt, K) * 512;
 }
 
@@ -381,6 +381,7 @@ w4_status fp4_dequantize(const w4_fp4 *a, void *out, int type, long long ldo, vo
 
 w4_status fp4_tile_scales(int fmt, int rows, int K, const uint8_t *row_scales, uint8_t *scales, void *stream) {
     if (!is_fp4(fmt) || rows < 1 || K < 32 || K % 32 || !row_scales || !scales) return W4_ERR_ARG;
+    if (too_large(rows, K)) return W4_ERR_UNSUPPORTED;
     if (!aligned16(row_scales) || !aligned16(scales)) return W4_ERR_ALIGN;
     const int tiles_k = fp4::scale_tiles_k(fmt, K);
     const long long blocks = ((long long)rows * tiles_k + 255) / 256;

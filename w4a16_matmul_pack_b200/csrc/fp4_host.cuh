@@ -20,6 +20,10 @@ inline bool rows16(long long ld, int type) { return ld * type_size(type) % 16 ==
 
 constexpr long long kMaxBlocks = 0x7FFFFFFFll;
 
+// Rows and K of an operand: with a tile (256) added they still fit an int.
+constexpr int kMaxExtent = 0x7FFFFFFF - 255;
+inline bool too_large(int rows, int K) { return rows > kMaxExtent || K > kMaxExtent; }
+
 // SMs of the current device (asked once per device; threads that ask at once read the same).
 inline w4_status device_sms(int &sms) {
     constexpr int kMaxDevices = 64;
@@ -35,6 +39,7 @@ inline w4_status device_sms(int &sms) {
 
 inline w4_status check_operand(const w4_fp4 *a) {
     if (!a || !is_fp4(a->fmt) || a->rows < 1 || a->K < 32 || a->K % 32 || !a->codes || !a->scales) return W4_ERR_ARG;
+    if (too_large(a->rows, a->K)) return W4_ERR_UNSUPPORTED;
     if (a->fmt == W4_FMT_NVFP4 && !a->global_scale) return W4_ERR_ARG;
     if (!aligned16(a->codes) || !aligned16(a->scales) || !aligned4(a->global_scale)) return W4_ERR_ALIGN;
     return W4_OK;
@@ -44,6 +49,7 @@ inline w4_status check_operand(const w4_fp4 *a) {
 inline w4_status check_quantised(int rows, int K, int fmt, int scale_rule, const float *global_scale, const uint8_t *codes,
                           const uint8_t *scales, const int *d_status) {
     if (!is_fp4(fmt) || rows < 1 || K < 32 || K % 32 || !codes || !scales) return W4_ERR_ARG;
+    if (too_large(rows, K)) return W4_ERR_UNSUPPORTED;
     if (scale_rule != W4_MX_SCALE_FLOOR && scale_rule != W4_MX_SCALE_CEIL) return W4_ERR_ARG;
     if (fmt == W4_FMT_NVFP4 && (!global_scale || scale_rule != W4_MX_SCALE_FLOOR)) return W4_ERR_ARG;
     if (!aligned16(codes) || !aligned16(scales) || !aligned4(global_scale) || !aligned4(d_status)) return W4_ERR_ALIGN;
