@@ -80,3 +80,26 @@ def test_a_pair_that_gives_up_frees_no_more_stages(fmt, M, N, K):
         W4.set_wait_limit(0)
         assert torch.equal(W4.w4a4_gemm(w, x, out=out), want)
         assert W4.w4_device_error(clear=True) == 0
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("M,N,K", [(1, 2560, 2560), (9, 2560, 9728), (16, 20000, 2560), (100, 512, 2560), (300, 1000, 4096)])
+def test_expired_waits_of_the_linear_layer(fmt, M, N, K):
+    """The same through w4a4_linear: up to 16 tokens the product's warps that quantise x
+    leave their ring, in its first round and in later ones."""
+    g = torch.tensor([0.002], device="cuda") if fmt == "nvfp4" else None
+    gen = torch.Generator(device="cuda").manual_seed(M)
+    x = torch.randn(M, K, generator=gen, device="cuda").bfloat16()
+    w = W4.fp4_quantize(torch.randn(N, K, generator=gen, device="cuda").bfloat16(), fmt, global_scale=g)
+    want = W4.w4a4_linear(w, x, global_scale=g)
+    torch.cuda.synchronize()
+    for _ in range(2):
+        W4.set_wait_limit(1)
+        t = time.monotonic()
+        W4.w4a4_linear(w, x, global_scale=g)
+        torch.cuda.synchronize()
+        assert time.monotonic() - t < 30
+        assert W4.w4_device_error(clear=True) == W4_ERR_TIMEOUT
+        W4.set_wait_limit(0)
+        assert torch.equal(W4.w4a4_linear(w, x, global_scale=g), want)
+        assert W4.w4_device_error(clear=True) == 0

@@ -314,3 +314,42 @@ def test_rows_and_columns_past_many_tiles():
     mr, nr = np.array([0, 1, 127, 128, 9999, 19998, 19999]), np.array([0, 5, 255, 256, 55555, 109998, 109999])
     got = y[torch.from_numpy(mr).cuda()][:, torch.from_numpy(nr).cuda()]
     check(got, xv[mr], wv[nr], torch.bfloat16)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M", [1, 9, 300])
+def test_the_normalised_result_of_a_layer(fmt, M):
+    """The second block norm of a layer: z too, within test_gpu_block_norm's bound."""
+    D, F = 512, 1376
+    y, h = randn(M, D, seed=1).cuda(), randn(M, D, seed=2, scale=2.0).cuda()
+    w1, _ = operand(randn(F, D, seed=3, scale=0.05), fmt)
+    w2, _ = operand(randn(D, F, seed=4, scale=0.03), fmt)
+    post, pre = ((1 + randn(D, seed=s, scale=0.1).float()).to(torch.bfloat16).cuda() for s in (5, 6))
+    g = torch.tensor([6.0 / 2688], device="cuda") if fmt == "nvfp4" else None
+    h1, z = W4.block_norm(y, h, post_weight=post, pre_weight=pre, quantize=fmt, global_scale=g)
+    act = torch.relu(W4.w4a4_gemm(w1, z))
+    down = W4.w4a4_linear(w2, act, global_scale=scale_of(act) if fmt == "nvfp4" else None)
+    h2, z2 = W4.block_norm(down, h1, post_weight=post, pre_weight=pre)
+    hn, zn = R.block_norm(R.f64(down), R.f64(h1), R.f64(post), R.f64(pre), None, None, 1, 1.0, 1.0,
+                          float(np.float32(1e-6)), 0.0)
+    size = np.abs(hn - R.f64(h1)) + np.abs(R.f64(h1))
+    assert np.all(np.abs(R.f64(h2) - hn) <= 2.0 ** -18 * size + R.half_step(hn, torch.bfloat16) * 1.01)
+    zsize = size / np.sqrt((hn * hn).mean(1, keepdims=True) + 1e-6) * np.abs(R.f64(pre))
+    assert np.all(np.abs(R.f64(z2) - zn) <= 2.0 ** -17 * zsize + R.half_step(zn, torch.bfloat16) * 1.01)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("K,N", [(2560, 9728), (9728, 2560), (2560, 20000), (4128, 19100)])
+def test_fused_linear_goes_round_its_ring(fmt, K, N):
+    """Up to 16 tokens with more stages of 256 k in a slice than the ring holds (5 in MXFP4,
+    4 in NVFP4): up to four rounds and five, the last ragged; the same bits as quantising
+    first, whose product goes by other loads."""
+    w = W4.fp4_quantize(torch.randn(N, K, generator=torch.Generator("cuda").manual_seed(K), device="cuda").bfloat16(), fmt,
+                        global_scale=torch.tensor([0.002], device="cuda") if fmt == "nvfp4" else None)
+    for M, dtype in ((1, torch.bfloat16), (1, torch.float32), (9, torch.bfloat16), (9, torch.float16),
+                     (16, torch.bfloat16), (16, torch.float32)):
+        x = randn(M, K, seed=M).to(dtype).cuda()
+        x[:, ::160] *= 30
+        g = scale_of(x) if fmt == "nvfp4" else None
+        y = W4.w4a4_linear(w, x, global_scale=g, out_dtype=torch.float32)
+        assert torch.equal(y, W4.w4a4_gemm(w, W4.fp4_quantize(x, fmt, global_scale=g), out_dtype=torch.float32)), (M, dtype)
