@@ -192,3 +192,63 @@ def test_deterministic_and_captured():
         out_h.zero_(), out.zero_()
         graph.replay()
         assert torch.equal(out_h, h0) and torch.equal(out, z0)
+
+
+def act_tolerance(g, act):
+    """Relative error of act(g).  sigmoid: the argument of 2^x is off by |g| log2(e)
+    (2^-24 + 2^-26) (its rounding and the constant's), which ln 2 turns into |g| 1.25 * 2^-24
+    of the power; the power and the division cost 2^-22 each, the sum 2^-24.  tanh from 0.3
+    on, 1 - q with q = 2 / (1 + 2^x): q is off by as much with 2 |g| for |g|, and q <= 2.44
+    tanh there; 2.44 (0.6 * 1.25 * 2^-24 + 2^-21 + 2^-24) < 2^-19 at 0.3 and less further
+    out.  Below: the series' next term 2^-24 and five roundings."""
+    return np.minimum(np.abs(g), 1e3) * 1.25 * 2.0 ** -24 + 2.0 ** -20 if act == "sigmoid" else np.full_like(g, 2.0 ** -19)
+
+
+@pytest.mark.parametrize("act", ["sigmoid", "tanh"])
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("own_rows", [False, True])
+def test_gates_far_from_zero(act, dtype, own_rows):
+    """Gates of both signs from 2^-20 to 200, beside tanh's border at 0.3, zeros of both
+    signs, and infinities.  sigmoid below 2^-126 is 0."""
+    D, M = 96, 4
+    border = np.float32(0.3)
+    mags = [0.0, 2.0 ** -20, 1e-3, 0.05, 0.29, np.nextafter(border, np.float32(0)), border,
+            np.nextafter(border, np.float32(1)), 0.2988, 0.3008, 0.31, 0.5, 1, 2, 4, 8, 9.5, 10, 12, 16, 17, 20, 30, 44, 60,
+            80, 86, 87, 87.5, 88, 88.75, 89, 95, 100, 103, 104, 120, 150, 200, np.inf]
+    g = np.zeros(D)
+    g[:2 * len(mags)] = np.concatenate([mags, np.negative(mags)])
+    gate = torch.from_numpy(np.stack([g, g[::-1], np.roll(g, 7), np.roll(g, 40)]) if own_rows else g[None]).to(dtype).cuda()
+    s = make(M, D, dtype, 5, post=False)
+    s["gate"], rows = gate, 1 if own_rows else M
+    h, z = call(s, gate_act=act, gate_rows=rows, block_scale=0.5)
+    h1, _ = W4.block_norm(s["y"], gate=gate, gate_act=act, gate_rows=rows, block_scale=0.5)    # the gated term alone
+    gv, yv = R.f64(gate)[np.arange(M) // rows], R.f64(s["y"])
+    with np.errstate(over="ignore"):
+        a = 1 / (1 + np.exp(-gv)) if act == "sigmoid" else np.tanh(gv)
+    b = 0.5 * a * yv
+    tol = (act_tolerance(gv, act) + 2.0 ** -23) * np.abs(b) + 2.0 ** -126 * np.abs(yv)
+    assert np.all(np.abs(R.f64(h1) - b) <= tol + R.half_step(b, dtype) * 1.01)
+    hv = R.f64(s["h"])
+    hn = hv + b
+    htol = tol + 2.0 ** -23 * (np.abs(hv) + np.abs(b))
+    assert np.all(np.abs(R.f64(h) - hn) <= htol + R.half_step(hn, dtype) * 1.01)
+    ms = (hn * hn).mean(1, keepdims=True) + 1e-6
+    r = 1 / np.sqrt(ms)
+    # the factor's relative error: that of half the mean square, whose sum is at most 64 additions deep
+    rtol = (htol * np.abs(hn)).mean(1, keepdims=True) / ms + 36 * 2.0 ** -24
+    zn = hn * r * R.f64(s["pre"])
+    ztol = htol * r * np.abs(R.f64(s["pre"])) + (rtol + 2.0 ** -22) * np.abs(zn)
+    assert np.all(np.abs(R.f64(z) - zn) <= ztol + R.half_step(zn, dtype) * 1.01)
+
+
+@pytest.mark.parametrize("act", ["none", "sigmoid", "tanh"])
+@pytest.mark.parametrize("own_rows", [False, True])
+def test_a_nan_gate_stays_in_its_rows(act, own_rows):
+    M, D = 3, 64
+    s = make(M, D, torch.float32, 6, gate_rows=1 if own_rows else M)
+    s["gate"][-1, 9] = float("nan")
+    h, z = call(s, gate_act=act, gate_rows=1 if own_rows else M)
+    bad = np.zeros((M, D), bool)
+    bad[M - 1 if own_rows else slice(None), 9] = True
+    assert np.array_equal(np.isnan(R.f64(h)), bad)
+    assert np.array_equal(np.isnan(R.f64(z)), np.broadcast_to(bad.any(1, keepdims=True), (M, D)))

@@ -171,7 +171,8 @@ __device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
 
 // act(gate).
 //   sigmoid: 1 / (1 + 2^(-g log2 e)); the argument's rounding costs |g| 2^-24, the
-//   exponential and the division 2^-22 each.
+//   exponential and the division 2^-22 each.  Below -87.3 the division gives 0 where
+//   sigmoid is less than 2^-126.
 //   tanh: from 0.3 on 1 - 2 / (1 + 2^(2 g log2 e)) (what the subtraction loses is at most
 //   two bits there); below, its Taylor series to g^9 (the next term is 5e-8 of the sum).
 // The library's tanhf inlined for every value of a row is code enough to make the
