@@ -1,6 +1,7 @@
 // common.cuh -- device helpers for the sm_100a kernels: format conversions,
 // mbarrier / bulk-copy PTX wrappers, bounded waits, programmatic dependent
-// launch.  Single translation unit: included once from w4a16.cu.
+// launch.  The error word and the wait limit are one copy per translation unit that
+// includes this.
 #pragma once
 
 #include <cuda.h>

@@ -271,7 +271,10 @@ w4_status few_tokens(const w4_fp4 *w, const w4_fp4 *x, void *y, long long ldy, i
     return launch_skinny<FMT, NT, T>(w, x, plain, y, ldy, out_type, s, early_w, st);
 }
 
-// The linear layer of at most kFusedTokens tokens in one kernel.
+// The linear layer of at most kFusedTokens tokens in one kernel: for a call by itself the
+// second launch costs the host 3.7 us, more than the GPU loses where it loses (nine NVFP4
+// tokens, 9728 x 2560: 8.6 us, as two launches 7.4; one token, 2560 x 9728 MXFP4 6.0 and
+// 6.6).
 constexpr int kFusedTokens = 16;
 
 template <int FMT>
